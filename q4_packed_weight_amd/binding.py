@@ -1,4 +1,5 @@
-"""Thin ctypes binding over libq4k.so (include/q4k.h, include/q4k_bench.h).
+"""Thin ctypes binding over libq4k.so (include/q4k.h, include/q4k_mx.h,
+include/q4k_bench.h).
 
 Argument marshalling only: every function takes torch tensors that already
 live on the GPU, passes their data pointers, sizes and the current torch
@@ -19,6 +20,11 @@ Q4K_ENULL = -2
 Q4K_EALIGN = -3
 Q4K_EHIP = -4
 Q4K_ESCRATCH = -5
+Q4K_EINVAL_TYPE = -6
+
+# Value types and block formats of the MX operators (include/q4k_mx.h).
+MX_TYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+MX_FORMAT = {"fp4": 4, "fp8": 8}
 
 EXPORTED = (
     "q4k_gemv", "q4k_matmul", "ternary_gemv_codes", "ternary_gemv", "ternary_matmul",
@@ -28,6 +34,8 @@ EXPORTED = (
     "q4k_matmul_tiled", "q4k_matmul_shaped", "q4k_matmul_tiled_shaped", "ternary_matmul_shaped",
     "q4k_matmul_noalloc",
     "q4k_strerror",
+    "mx_quantize", "mx_dequantize", "mx_rmsnorm", "mxfp4_matmul", "mxfp4_moe_workspace_size",
+    "mxfp4_moe",
     "q4k_bench_empty", "q4k_bench_delay", "q4k_bench_stream_read", "q4k_bench_copy",
 )
 
@@ -73,6 +81,11 @@ def lib():
         "q4k_matmul_tiled": [P, P, I64, I64, I64, P, P],
         "q4k_matmul_shaped": [P, P, I64, I64, I64, P, P, I],
         "q4k_matmul_tiled_shaped": [P, P, I64, I64, I64, P, P, I],
+        "mx_quantize": [P, I, I, I64, I64, P, P, P],
+        "mx_dequantize": [P, P, I, I64, I64, P, I, P],
+        "mx_rmsnorm": [P, P, P, F, I, I64, I64, P, P, I, P, P, P],
+        "mxfp4_matmul": [P, P, I, P, P, I64, I64, I64, P, I, P],
+        "mxfp4_moe": [P, I, P, P, P, P, P, P, I64, I64, I64, I64, I64, P, P, I64, P],
         "q4k_bench_empty": [P],
         "q4k_bench_delay": [I64, P],
         "q4k_bench_stream_read": [P, I64, P, I64, P],
@@ -84,6 +97,8 @@ def lib():
         f.restype = I
     L.q4k_tiled_size.argtypes = [I64, I64]
     L.q4k_tiled_size.restype = I64
+    L.mxfp4_moe_workspace_size.argtypes = [I64, I64, I64, I64, I64]
+    L.mxfp4_moe_workspace_size.restype = I64
     L.q4k_strerror.argtypes = [I]
     L.q4k_strerror.restype = ctypes.c_char_p
     _lib = L
@@ -359,6 +374,115 @@ def ternary_matmul_shaped(X, codes, scale, n_tokens, input_dim, output_dim, Y, f
     _check(lib().ternary_matmul_shaped(_ptr(X), _ptr(codes), float(scale), M, K, N, _ptr(Y),
                                        _stream(stream), int(form)), "ternary_matmul_shaped")
     return Y
+
+
+def _mx_type(t, name):
+    if t is None:
+        raise ValueError(f"{name} is required")
+    code = MX_TYPE.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    return code
+
+
+def _mx_format(fmt):
+    code = MX_FORMAT.get(fmt)
+    if code is None:
+        raise ValueError(f"MX format must be 'fp4' or 'fp8', got {fmt!r}")
+    return code
+
+
+def _mx_codes(codes, scales, fmt, rows, K, what):
+    """Marshalling checks of a matrix in MX blocks."""
+    n = rows * K if rows > 0 and K > 0 and K % 32 == 0 else 0
+    _expect(codes, torch.uint8, f"{what}codes", n // 2 if fmt == "fp4" else n)
+    _expect(scales, torch.uint8, f"{what}scales", n // 32)
+
+
+def _mx_values(t, dtype, name, rows, K):
+    _expect(t, dtype, name, rows * K if rows > 0 and K > 0 else 0)
+
+
+def mx_quantize(x, n_rows, input_dim, fmt, codes, scales, stream=None):
+    """Rows of x (fp32, bf16 or fp16) to MX blocks; fmt is "fp4" or "fp8"."""
+    R, K = int(n_rows), int(input_dim)
+    t, f = _mx_type(x, "x"), _mx_format(fmt)
+    _mx_values(x, x.dtype, "x", R, K)
+    _mx_codes(codes, scales, fmt, R, K, "")
+    _check(lib().mx_quantize(_ptr(x), t, f, R, K, _ptr(codes), _ptr(scales), _stream(stream)),
+           "mx_quantize")
+    return codes, scales
+
+
+def mx_dequantize(codes, scales, n_rows, input_dim, fmt, y, stream=None):
+    """The values of MX blocks, rounded to y's type."""
+    R, K = int(n_rows), int(input_dim)
+    t, f = _mx_type(y, "y"), _mx_format(fmt)
+    _mx_codes(codes, scales, fmt, R, K, "")
+    _mx_values(y, y.dtype, "y", R, K)
+    _check(lib().mx_dequantize(_ptr(codes), _ptr(scales), f, R, K, _ptr(y), t, _stream(stream)),
+           "mx_dequantize")
+    return y
+
+
+def mx_rmsnorm(x, residual, weight, eps, n_rows, input_dim, fmt, residual_out, y, codes, scales,
+               stream=None):
+    """Residual addition and RMS norm with MX blocks out; residual,
+    residual_out, y, and codes with scales (fmt then unused) may be None."""
+    R, K = int(n_rows), int(input_dim)
+    t = _mx_type(x, "x")
+    f = _mx_format(fmt) if codes is not None or scales is not None else 0
+    _mx_values(x, x.dtype, "x", R, K)
+    _mx_values(residual, x.dtype, "residual", R, K)
+    _mx_values(weight, x.dtype, "weight", 1, K)
+    _mx_values(residual_out, x.dtype, "residual_out", R, K)
+    _mx_values(y, x.dtype, "y", R, K)
+    _mx_codes(codes, scales, fmt, R, K, "")
+    _check(lib().mx_rmsnorm(_ptr(x), _ptr(residual), _ptr(weight), float(eps), t, R, K,
+                            _ptr(residual_out), _ptr(y), f, _ptr(codes), _ptr(scales),
+                            _stream(stream)), "mx_rmsnorm")
+    return codes, scales
+
+
+def mxfp4_matmul(a_codes, a_scales, a_fmt, w_codes, w_scales, n_tokens, input_dim, output_dim, Y,
+                 stream=None):
+    """Y = A W^T of MX activations (a_fmt "fp8" or "fp4") and MXFP4 weights."""
+    M, K, N = int(n_tokens), int(input_dim), int(output_dim)
+    t, f = _mx_type(Y, "Y"), _mx_format(a_fmt)
+    _mx_codes(a_codes, a_scales, a_fmt, M, K, "a_")
+    _mx_codes(w_codes, w_scales, "fp4", N, K, "w_")
+    _mx_values(Y, Y.dtype, "Y", M, N)
+    _check(lib().mxfp4_matmul(_ptr(a_codes), _ptr(a_scales), f, _ptr(w_codes), _ptr(w_scales),
+                              M, K, N, _ptr(Y), t, _stream(stream)), "mxfp4_matmul")
+    return Y
+
+
+def mxfp4_moe_workspace_size(n_tokens, input_dim, ffn_dim, n_experts, top_k):
+    """Bytes of mxfp4_moe's workspace (raises on invalid dimensions)."""
+    n = lib().mxfp4_moe_workspace_size(int(n_tokens), int(input_dim), int(ffn_dim),
+                                       int(n_experts), int(top_k))
+    _check(n if n < 0 else Q4K_OK, "mxfp4_moe_workspace_size")
+    return n
+
+
+def mxfp4_moe(x, router, router_bias, up_codes, up_scales, down_codes, down_scales, n_tokens,
+              input_dim, ffn_dim, n_experts, top_k, y, workspace, stream=None):
+    """A mixture-of-experts layer with MXFP4 experts; router_bias may be None."""
+    T, H, F, E, k = int(n_tokens), int(input_dim), int(ffn_dim), int(n_experts), int(top_k)
+    t = _mx_type(x, "x")
+    _mx_values(x, x.dtype, "x", T, H)
+    _mx_values(router, x.dtype, "router", E, H)
+    _expect(router_bias, torch.float32, "router_bias", max(E, 0))
+    _mx_codes(up_codes, up_scales, "fp4", E * 2 * F, H, "up_")
+    _mx_codes(down_codes, down_scales, "fp4", E * H, F, "down_")
+    _mx_values(y, x.dtype, "y", T, H)
+    _expect(workspace, torch.uint8, "workspace")
+    _check(lib().mxfp4_moe(_ptr(x), t, _ptr(router), _ptr(router_bias), _ptr(up_codes),
+                           _ptr(up_scales), _ptr(down_codes), _ptr(down_scales), T, H, F, E, k,
+                           _ptr(y), _ptr(workspace),
+                           0 if workspace is None else workspace.numel(), _stream(stream)),
+           "mxfp4_moe")
+    return y
 
 
 def bench_empty(stream=None):

@@ -1,0 +1,42 @@
+// mx_internal.h -- launchers of the microscaled (MX) kernels.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace q4k {
+
+hipError_t mx_quantize_launch(const void *x, int type, int format, int64_t n_rows, int64_t K,
+                              uint8_t *codes, uint8_t *scales, hipStream_t stream);
+hipError_t mx_dequantize_launch(const uint8_t *codes, const uint8_t *scales, int format,
+                                int64_t n_rows, int64_t K, void *y, int type, hipStream_t stream);
+// format 0: no codes.
+hipError_t mx_rmsnorm_launch(const void *x, const void *residual, const void *weight, float eps,
+                             int type, int64_t n_rows, int64_t K, void *residual_out, void *y,
+                             int format, uint8_t *codes, uint8_t *scales, hipStream_t stream);
+hipError_t mxfp4_matmul_launch(const uint8_t *a, const uint8_t *as, int a_format,
+                               const uint8_t *w, const uint8_t *ws, int64_t M, int64_t K,
+                               int64_t N, void *Y, int type, hipStream_t stream);
+
+// The mixture-of-experts layer works on at most kMoeTokens tokens at a time,
+// and on no more than keep its logits in 32 KiB of LDS.
+constexpr int kMoeTokens = 64;
+constexpr int kMoeMaxLogits = 8192;
+inline int64_t moe_tokens_at_once(int64_t E) {
+  return kMoeMaxLogits / E < kMoeTokens ? kMoeMaxLogits / E : kMoeTokens;
+}
+constexpr int kMoeMaxExperts = 256;
+constexpr int kMoeMaxTopK = 16;
+struct MoeArgs {
+  const void *x;
+  const void *router;
+  const float *bias;
+  const uint8_t *up, *up_s, *down, *down_s;
+  void *y;
+  void *workspace;
+  int type, T, H, F, E, k;  // T <= moe_tokens_at_once(E)
+};
+int64_t moe_workspace_bytes(int64_t T, int64_t H, int64_t F, int64_t E, int64_t k);
+hipError_t mxfp4_moe_launch(const MoeArgs &a, hipStream_t stream);
+
+}  // namespace q4k

@@ -1,0 +1,159 @@
+// mx_rmsnorm.hip -- residual addition, root-mean-square norm, MX blocks out.
+#include "mx_common.h"
+#include "mx_internal.h"
+
+namespace q4k {
+namespace {
+
+// Sum of one value per thread over the workgroup, in every thread: within a
+// wave by cross-lane adds, then the waves' sums in order.
+__device__ __forceinline__ float block_sum(float v, float *lds) {
+  v = group_sum<64>(v);
+  const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  if ((threadIdx.x & 63) == 0) lds[wave] = v;
+  __syncthreads();
+  float t = 0.0f;
+  for (int i = 0; i < waves; i++) t += lds[i];
+  return t;
+}
+
+// The sum the norm is taken of: x + residual rounded to the type, so that the
+// next layer's residual is the vector this norm saw.
+template <int T>
+__device__ __forceinline__ Raw8<T> add_raw8(const Raw8<T> &a, const Raw8<T> &b) {
+  float f[8], g[8];
+  raw8_to_f32<T>(a, f);
+  raw8_to_f32<T>(b, g);
+#pragma unroll
+  for (int i = 0; i < 8; i++) f[i] += g[i];
+  return f32_to_raw8<T>(f);
+}
+
+template <int T>
+__device__ __forceinline__ float sum_squares(const Raw8<T> &r) {
+  float f[8], s = 0.0f;
+  raw8_to_f32<T>(r, f);
+#pragma unroll
+  for (int i = 0; i < 8; i++) s = __builtin_fmaf(f[i], f[i], s);
+  return s;
+}
+
+// Eight normed values: y and the codes of their block.
+template <int T>
+__device__ __forceinline__ void emit8(const Raw8<T> &r, const Raw8<T> &w, float inv, int64_t chunk,
+                                      void *y, int format, uint8_t *codes, uint8_t *scales) {
+  float f[8], g[8];
+  raw8_to_f32<T>(r, f);
+  raw8_to_f32<T>(w, g);
+#pragma unroll
+  for (int i = 0; i < 8; i++) f[i] = f[i] * inv * g[i];
+  if (y) store_raw8<T>(y, chunk, f32_to_raw8<T>(f));
+  if (format == MX_FP8) {
+    const uint32_t s = mx_scale_byte<MX_FP8>(block_amax_bits(f));
+    reinterpret_cast<u32x2 *>(codes)[chunk] = mx_encode8<MX_FP8>(f, s);
+    if ((chunk & 3) == 0) scales[chunk >> 2] = (uint8_t)s;
+  } else if (format == MX_FP4) {
+    const uint32_t s = mx_scale_byte<MX_FP4>(block_amax_bits(f));
+    reinterpret_cast<uint32_t *>(codes)[chunk] = mx_encode8<MX_FP4>(f, s)[0];
+    if ((chunk & 3) == 0) scales[chunk >> 2] = (uint8_t)s;
+  }
+}
+
+// One row per workgroup, held in registers as NC chunks of eight values per
+// lane, so memory is read once; four neighbouring lanes hold one block.
+template <int T, int NC>
+__global__ __launch_bounds__(1024) void mx_rmsnorm_kernel(const void *x, const void *residual,
+                                                          const void *weight, float eps, int n,
+                                                          float inv_dim, void *residual_out,
+                                                          void *y, int format, uint8_t *codes,
+                                                          uint8_t *scales) {
+  __shared__ float lds[16];
+  const int64_t base = (int64_t)blockIdx.x * n;  // chunk index of the row's first
+  Raw8<T> r[NC], w[NC];
+#pragma unroll
+  for (int j = 0; j < NC; j++) {
+    const int c = threadIdx.x + j * blockDim.x;
+    if (c < n) {
+      r[j] = load_raw8<T>(x, base + c);
+      if (residual) w[j] = load_raw8<T>(residual, base + c);
+    }
+  }
+  float ss = 0.0f;
+#pragma unroll
+  for (int j = 0; j < NC; j++) {
+    const int c = threadIdx.x + j * blockDim.x;
+    if (c < n) {
+      if (residual) r[j] = add_raw8<T>(r[j], w[j]);
+      ss += sum_squares<T>(r[j]);
+      w[j] = load_raw8<T>(weight, c);
+    }
+  }
+  const float inv = 1.0f / __builtin_sqrtf(block_sum(ss, lds) * inv_dim + eps);
+#pragma unroll
+  for (int j = 0; j < NC; j++) {
+    const int c = threadIdx.x + j * blockDim.x;
+    if (c < n) {
+      if (residual_out) store_raw8<T>(residual_out, base + c, r[j]);
+      emit8<T>(r[j], w[j], inv, base + c, y, format, codes, scales);
+    }
+  }
+}
+
+// Rows too long for registers: one pass for the sum, one for the outputs.
+// Each lane writes only the chunks of residual_out that it reads again
+// itself, so residual_out may be x or residual.
+template <int T>
+__global__ __launch_bounds__(1024) void mx_rmsnorm_long_kernel(
+    const void *x, const void *residual, const void *weight, float eps, int n, float inv_dim,
+    void *residual_out, void *y, int format, uint8_t *codes, uint8_t *scales) {
+  __shared__ float lds[16];
+  const int64_t base = (int64_t)blockIdx.x * n;
+  float ss = 0.0f;
+  for (int c = threadIdx.x; c < n; c += blockDim.x) {
+    Raw8<T> r = load_raw8<T>(x, base + c);
+    if (residual) r = add_raw8<T>(r, load_raw8<T>(residual, base + c));
+    ss += sum_squares<T>(r);
+  }
+  const float inv = 1.0f / __builtin_sqrtf(block_sum(ss, lds) * inv_dim + eps);
+  for (int c = threadIdx.x; c < n; c += blockDim.x) {
+    Raw8<T> r = load_raw8<T>(x, base + c);
+    if (residual) r = add_raw8<T>(r, load_raw8<T>(residual, base + c));
+    if (residual_out) store_raw8<T>(residual_out, base + c, r);
+    emit8<T>(r, load_raw8<T>(weight, c), inv, base + c, y, format, codes, scales);
+  }
+}
+
+}  // namespace
+
+hipError_t mx_rmsnorm_launch(const void *x, const void *residual, const void *weight, float eps,
+                             int type, int64_t n_rows, int64_t K, void *residual_out, void *y,
+                             int format, uint8_t *codes, uint8_t *scales, hipStream_t stream) {
+  const int n = (int)(K / 8);
+  const float inv_dim = 1.0f / (float)K;
+  // chunks per lane: one up to 1024 chunks, two, then four
+  const int nc = n <= 1024 ? 1 : n <= 2048 ? 2 : 4;
+  const int lanes = (n + nc - 1) / nc;
+  const int threads = lanes >= 1024 ? 1024 : (lanes + 63) / 64 * 64;
+  // Rows beyond 2^31 - 1 of a grid never occur: their codes alone would not
+  // fit the GPU.
+#define ARGS x, residual, weight, eps, n, inv_dim, residual_out, y, format, codes, scales
+#define CALL(T)                                                                                   \
+  if (n > 4096)                                                                                   \
+    hipLaunchKernelGGL((mx_rmsnorm_long_kernel<T>), dim3(n_rows), dim3(1024), 0, stream, ARGS);   \
+  else if (nc == 1)                                                                               \
+    hipLaunchKernelGGL((mx_rmsnorm_kernel<T, 1>), dim3(n_rows), dim3(threads), 0, stream, ARGS);  \
+  else if (nc == 2)                                                                               \
+    hipLaunchKernelGGL((mx_rmsnorm_kernel<T, 2>), dim3(n_rows), dim3(threads), 0, stream, ARGS);  \
+  else                                                                                            \
+    hipLaunchKernelGGL((mx_rmsnorm_kernel<T, 4>), dim3(n_rows), dim3(threads), 0, stream, ARGS)
+  switch (type) {
+    case MX_F32: CALL(MX_F32); break;
+    case MX_BF16: CALL(MX_BF16); break;
+    default: CALL(MX_F16); break;
+  }
+#undef CALL
+#undef ARGS
+  return hipGetLastError();
+}
+
+}  // namespace q4k

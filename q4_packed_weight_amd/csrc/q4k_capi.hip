@@ -7,8 +7,10 @@
 #include <mutex>
 #include <vector>
 
+#include "mx_internal.h"
 #include "q4k.h"
 #include "q4k_internal.h"
+#include "q4k_mx.h"
 
 namespace {
 
@@ -158,6 +160,25 @@ bool valid_vector_shape(int rows_per_lane, int k_waves, int workgroup_waves) {
     return false;
   const int wg = workgroup_waves ? workgroup_waves : 4;
   return !(k_waves > wg || (wg == 8 && (k_waves == 4 || rows_per_lane == 8)));
+}
+
+// Dimensions common to the MX entry points: rows counted by a grid, whole
+// blocks of 32 values.
+bool valid_mx_dims(int64_t rows, int64_t K) {
+  return rows > 0 && rows <= 0x7FFFFFFF && K > 0 && K % 32 == 0 && K <= kMaxInputDim;
+}
+bool valid_mx_type(int t) { return t == MX_F32 || t == MX_BF16 || t == MX_F16; }
+bool valid_mx_format(int f) { return f == MX_FP4 || f == MX_FP8; }
+
+// Largest n_tokens of mxfp4_matmul (64 tokens a workgroup, 65535 of them in
+// a grid's second dimension) and input_dim / ffn_dim of mxfp4_moe.
+constexpr int64_t kMaxMxTokens = (int64_t)1 << 21;
+constexpr int64_t kMaxMoeDim = (int64_t)1 << 20;
+
+bool valid_moe_dims(int64_t T, int64_t H, int64_t F, int64_t E, int64_t k) {
+  return T > 0 && T <= kMaxMxTokens && H > 0 && H % 32 == 0 && H <= kMaxMoeDim && F > 0 &&
+         F % 32 == 0 && F <= kMaxMoeDim && E > 0 && E <= q4k::kMoeMaxExperts && k > 0 && k <= E &&
+         k <= q4k::kMoeMaxTopK;
 }
 
 }  // namespace
@@ -538,15 +559,108 @@ int q4k_matmul_tiled(const float *X, const uint8_t *w_tiled, int64_t n_tokens, i
   return e == hipSuccess ? Q4K_OK : hip_fail(e, "q4k_matmul_tiled launch");
 }
 
+int mx_quantize(const void *x, int x_type, int format, int64_t n_rows, int64_t input_dim,
+                uint8_t *codes, uint8_t *scales, void *stream) {
+  if (!valid_mx_dims(n_rows, input_dim)) return Q4K_EINVAL_DIM;
+  if (!valid_mx_type(x_type) || !valid_mx_format(format)) return Q4K_EINVAL_TYPE;
+  if (!x || !codes || !scales) return Q4K_ENULL;
+  if (!aligned16(x) || !aligned16(codes)) return Q4K_EALIGN;
+  hipError_t e = q4k::mx_quantize_launch(x, x_type, format, n_rows, input_dim, codes, scales,
+                                         (hipStream_t)stream);
+  return e == hipSuccess ? Q4K_OK : hip_fail(e, "mx_quantize launch");
+}
+
+int mx_dequantize(const uint8_t *codes, const uint8_t *scales, int format, int64_t n_rows,
+                  int64_t input_dim, void *y, int y_type, void *stream) {
+  if (!valid_mx_dims(n_rows, input_dim)) return Q4K_EINVAL_DIM;
+  if (!valid_mx_type(y_type) || !valid_mx_format(format)) return Q4K_EINVAL_TYPE;
+  if (!codes || !scales || !y) return Q4K_ENULL;
+  if (!aligned16(codes) || !aligned16(y)) return Q4K_EALIGN;
+  hipError_t e = q4k::mx_dequantize_launch(codes, scales, format, n_rows, input_dim, y, y_type,
+                                           (hipStream_t)stream);
+  return e == hipSuccess ? Q4K_OK : hip_fail(e, "mx_dequantize launch");
+}
+
+int mx_rmsnorm(const void *x, const void *residual, const void *weight, float eps, int type,
+               int64_t n_rows, int64_t input_dim, void *residual_out, void *y, int format,
+               uint8_t *codes, uint8_t *scales, void *stream) {
+  if (!valid_mx_dims(n_rows, input_dim) || !(eps >= 0.0f)) return Q4K_EINVAL_DIM;
+  const bool blocks = codes || scales;
+  if (!valid_mx_type(type) || (blocks && !valid_mx_format(format))) return Q4K_EINVAL_TYPE;
+  if (!x || !weight || (blocks && (!codes || !scales)) || (!blocks && !y && !residual_out))
+    return Q4K_ENULL;
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(residual_out) ||
+      !aligned16(y) || !aligned16(codes))
+    return Q4K_EALIGN;
+  hipError_t e = q4k::mx_rmsnorm_launch(x, residual, weight, eps, type, n_rows, input_dim,
+                                        residual_out, y, blocks ? format : 0, codes, scales,
+                                        (hipStream_t)stream);
+  return e == hipSuccess ? Q4K_OK : hip_fail(e, "mx_rmsnorm launch");
+}
+
+int mxfp4_matmul(const uint8_t *a_codes, const uint8_t *a_scales, int a_format,
+                 const uint8_t *w_codes, const uint8_t *w_scales, int64_t n_tokens,
+                 int64_t input_dim, int64_t output_dim, void *Y, int y_type, void *stream) {
+  if (!valid_mx_dims(output_dim, input_dim) || n_tokens <= 0 || n_tokens > kMaxMxTokens)
+    return Q4K_EINVAL_DIM;
+  if (!valid_mx_format(a_format) || !valid_mx_type(y_type)) return Q4K_EINVAL_TYPE;
+  if (!a_codes || !a_scales || !w_codes || !w_scales || !Y) return Q4K_ENULL;
+  if (!aligned16(a_codes) || !aligned16(w_codes)) return Q4K_EALIGN;
+  hipError_t e = q4k::mxfp4_matmul_launch(a_codes, a_scales, a_format, w_codes, w_scales, n_tokens,
+                                          input_dim, output_dim, Y, y_type, (hipStream_t)stream);
+  return e == hipSuccess ? Q4K_OK : hip_fail(e, "mxfp4_matmul launch");
+}
+
+int64_t mxfp4_moe_workspace_size(int64_t n_tokens, int64_t input_dim, int64_t ffn_dim,
+                                 int64_t n_experts, int64_t top_k) {
+  if (!valid_moe_dims(n_tokens, input_dim, ffn_dim, n_experts, top_k)) return Q4K_EINVAL_DIM;
+  return q4k::moe_workspace_bytes(n_tokens, input_dim, ffn_dim, n_experts, top_k);
+}
+
+int mxfp4_moe(const void *x, int type, const void *router, const float *router_bias,
+              const uint8_t *up_codes, const uint8_t *up_scales, const uint8_t *down_codes,
+              const uint8_t *down_scales, int64_t n_tokens, int64_t input_dim, int64_t ffn_dim,
+              int64_t n_experts, int64_t top_k, void *y, void *workspace, int64_t workspace_bytes,
+              void *stream) {
+  if (!valid_moe_dims(n_tokens, input_dim, ffn_dim, n_experts, top_k)) return Q4K_EINVAL_DIM;
+  if (!valid_mx_type(type)) return Q4K_EINVAL_TYPE;
+  if (!x || !router || !up_codes || !up_scales || !down_codes || !down_scales || !y || !workspace)
+    return Q4K_ENULL;
+  if (!aligned16(x) || !aligned16(router) || !aligned16(up_codes) || !aligned16(down_codes) ||
+      !aligned16(y) || ((uintptr_t)workspace & 255u) != 0 || ((uintptr_t)router_bias & 3u) != 0)
+    return Q4K_EALIGN;
+  if (workspace_bytes <
+      q4k::moe_workspace_bytes(n_tokens, input_dim, ffn_dim, n_experts, top_k)) {
+    snprintf(g_hip_detail, sizeof g_hip_detail,
+             "mxfp4_moe: the scratch workspace is smaller than mxfp4_moe_workspace_size");
+    return Q4K_ESCRATCH;
+  }
+  const int64_t most = q4k::moe_tokens_at_once(n_experts);
+  const int64_t row_bytes = input_dim * (type == MX_F32 ? 4 : 2);
+  for (int64_t t = 0; t < n_tokens; t += most) {
+    const int64_t n = n_tokens - t < most ? n_tokens - t : most;
+    const q4k::MoeArgs a{static_cast<const uint8_t *>(x) + t * row_bytes, router, router_bias,
+                         up_codes, up_scales, down_codes, down_scales,
+                         static_cast<uint8_t *>(y) + t * row_bytes, workspace, type, (int)n,
+                         (int)input_dim, (int)ffn_dim, (int)n_experts, (int)top_k};
+    hipError_t e = q4k::mxfp4_moe_launch(a, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "mxfp4_moe launch");
+  }
+  return Q4K_OK;
+}
+
 const char *q4k_strerror(int code) {
   switch (code) {
     case Q4K_OK: return "ok";
     case Q4K_EINVAL_DIM:
       return "invalid dimension: every dimension must be > 0, input_dim a "
-             "multiple of 256 for Q4_K, Q4_0 and Q6_K (of 4 for ternary) and at "
-             "most 2^24";
+             "multiple of 256 for Q4_K, Q4_0 and Q6_K (of 4 for ternary, of 32 for MX) "
+             "and at most 2^24";
     case Q4K_ENULL: return "a required pointer is NULL";
-    case Q4K_EALIGN: return "x and the Q4_K, Q4_0 or Q6_K blocks must be 16-byte aligned";
+    case Q4K_EALIGN:
+      return "x and the Q4_K, Q4_0 or Q6_K blocks must be 16-byte aligned (MX: values and codes "
+             "too, the workspace 256-byte aligned)";
+    case Q4K_EINVAL_TYPE: return "unknown value type or MX format";
     case Q4K_EHIP: return g_hip_detail[0] ? g_hip_detail : "HIP runtime error";
     case Q4K_ESCRATCH:
       return g_hip_detail[0] ? g_hip_detail
