@@ -177,37 +177,33 @@ template <int T> __device__ __forceinline__ void store_value(void *p, int64_t i,
   reinterpret_cast<typename MxStore<T>::type *>(p)[i] = (typename MxStore<T>::type)v;
 }
 
+// Keeps the registers of an operand alive until d is written.
+template <int F> __device__ __forceinline__ void keep_operand(f32x4 &d, i32x8 v) {
+  if constexpr (F == MX_FP4) {
+    const i32x4 lo = {v[0], v[1], v[2], v[3]};
+    asm("" : "+v"(d) : "v"(lo));
+  } else {
+    asm("" : "+v"(d) : "v"(v));
+  }
+}
+
 // D += A * B over 16 rows x 16 columns x 128 positions on the scaled matrix
 // instruction; A in format AF, B in BF.  Lane l holds row (column) l % 16 of
 // its operand and, with g = l / 16, the positions
 //   MX_FP4: 32g .. 32g+31 (16 bytes in the first four dwords)
 //   MX_FP8: 16g .. 16g+15 and 64+16g .. 64+16g+15 (the low and the high half)
-// and the scale byte of block g (positions 32g .. 32g+31) of its row in the
-// low byte of sa (sb); D has column l % 16, rows 4g .. 4g+3.  The instruction
+// and the scale byte of block g (positions 32g .. 32g+31) of its row in
+// byte J of sa (sb); D has column l % 16, rows 4g .. 4g+3.  The instruction
 // gives wrong sums when D lies on registers of A or B (seen with this
-// compiler, which allows it where an operand dies there): the empty statement
-// keeps both alive until D is written, at no instruction.
-template <int AF, int BF>
+// compiler, which allows it where an operand dies there): keep_operand holds
+// both until D is written, at no instruction.
+template <int AF, int BF, int J = 0>
 __device__ __forceinline__ f32x4 mfma_scaled(i32x8 a, i32x8 b, f32x4 d, int sa, int sb) {
   d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, d, AF == MX_FP4 ? 4 : 0,
-                                                       BF == MX_FP4 ? 4 : 0, 0, sa, 0, sb);
-  asm("" : "+v"(d) : "v"(a), "v"(b));
+                                                       BF == MX_FP4 ? 4 : 0, J, sa, J, sb);
+  keep_operand<AF>(d, a);
+  keep_operand<BF>(d, b);
   return d;
-}
-
-// One lane's bytes of a 128-position step of a row: `row` points at the
-// step's first byte and `blocks` of its four blocks exist (the others read as
-// zero codes; an FP8 lane holds halves of blocks g/2 and 2+g/2).
-template <int FMT>
-__device__ __forceinline__ i32x8 load_operand(const uint8_t *row, int g, int blocks) {
-  i32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
-  if constexpr (FMT == MX_FP4) {
-    if (g < blocks) lo = *reinterpret_cast<const i32x4 *>(row + 16 * g);
-  } else {
-    if ((g >> 1) < blocks) lo = *reinterpret_cast<const i32x4 *>(row + 16 * g);
-    if (2 + (g >> 1) < blocks) hi = *reinterpret_cast<const i32x4 *>(row + 64 + 16 * g);
-  }
-  return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
 }
 
 // e4m3 codes as two operands that add up to them: the values of 2 and above
@@ -228,15 +224,15 @@ __device__ __forceinline__ void split_e4m3(i32x8 v, i32x8 &high, i32x8 &low) {
 }
 
 // The product with all of fp32's accuracy (EXACT) or as the instruction adds.
-template <int AF, int BF, bool EXACT>
+template <int AF, int BF, bool EXACT, int J = 0>
 __device__ __forceinline__ f32x4 mfma_mx(i32x8 a, i32x8 b, f32x4 d, int sa, int sb) {
   if constexpr (EXACT && BF == MX_FP8) {
     i32x8 high, low;
     split_e4m3(b, high, low);
-    d = mfma_scaled<AF, BF>(a, low, d, sa, sb);
-    return mfma_scaled<AF, BF>(a, high, d, sa, sb);
+    d = mfma_scaled<AF, BF, J>(a, low, d, sa, sb);
+    return mfma_scaled<AF, BF, J>(a, high, d, sa, sb);
   } else {
-    return mfma_scaled<AF, BF>(a, b, d, sa, sb);
+    return mfma_scaled<AF, BF, J>(a, b, d, sa, sb);
   }
 }
 

@@ -17,6 +17,11 @@ hipError_t mx_rmsnorm_launch(const void *x, const void *residual, const void *we
 hipError_t mxfp4_matmul_launch(const uint8_t *a, const uint8_t *as, int a_format,
                                const uint8_t *w, const uint8_t *ws, int64_t M, int64_t K,
                                int64_t N, void *Y, int type, hipStream_t stream);
+// The form for many tokens; K <= kMxTiledMaxDim.
+constexpr int64_t kMxTiledMaxDim = (int64_t)1 << 22;
+hipError_t mxfp4_matmul_tiled_launch(const uint8_t *a, const uint8_t *as, int a_format,
+                                     const uint8_t *w, const uint8_t *ws, int64_t M, int64_t K,
+                                     int64_t N, void *Y, int type, hipStream_t stream);
 
 // The mixture-of-experts layer works on at most kMoeTokens tokens at a time,
 // and on no more than keep its logits in 32 KiB of LDS.
