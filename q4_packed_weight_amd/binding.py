@@ -106,15 +106,17 @@ def lib():
 
 
 def _ptr(t):
-    if t is None:
-        return None
-    return ctypes.c_void_p(t.data_ptr()) if t.numel() else ctypes.c_void_p(t.data_ptr() or 0)
+    return None if t is None else t.data_ptr()
+
+
+# The current stream's handle without a Stream object around it, which takes
+# longer to make than everything else here.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    return _raw_stream(_current_device()) if stream is None else stream.cuda_stream
 
 
 def _check(rc, func):
@@ -127,11 +129,11 @@ def _expect(t, dtype, name, need=0):
     dimensions imply (0 = not checked here, the C side validates dims)."""
     if t is None:
         return
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
     if need > 0 and t.numel() < need:
         raise ValueError(f"{name} has {t.numel()} elements, the dimensions need {need}")

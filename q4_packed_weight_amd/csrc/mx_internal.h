@@ -17,6 +17,10 @@ hipError_t mx_rmsnorm_launch(const void *x, const void *residual, const void *we
 hipError_t mxfp4_matmul_launch(const uint8_t *a, const uint8_t *as, int a_format,
                                const uint8_t *w, const uint8_t *ws, int64_t M, int64_t K,
                                int64_t N, void *Y, int type, hipStream_t stream);
+// Rows of whole 128-position steps whose scales start at dwords.
+inline bool mx_aligned_scales(const uint8_t *as, const uint8_t *ws, int64_t K) {
+  return K % 128 == 0 && ((reinterpret_cast<uintptr_t>(as) | reinterpret_cast<uintptr_t>(ws)) & 3) == 0;
+}
 // The form for many tokens; K <= kMxTiledMaxDim.
 constexpr int64_t kMxTiledMaxDim = (int64_t)1 << 22;
 hipError_t mxfp4_matmul_tiled_launch(const uint8_t *a, const uint8_t *as, int a_format,

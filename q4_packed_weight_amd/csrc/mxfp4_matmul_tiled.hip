@@ -1,87 +1,36 @@
 // mxfp4_matmul_tiled.hip -- the MX product for many tokens: tiles staged
 // through LDS for the scaled matrix instruction.
+#include <algorithm>
+#include <cmath>
 #include <type_traits>
 
-#include "mx_common.h"
 #include "mx_internal.h"
+#include "mx_lds.h"
 
 namespace q4k {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kStages = 3;
-
-// One 16-byte piece per lane from a buffer view straight into LDS: lane l's
-// lands at lds + 16 l, zeros where the offset is past the view's end.  The
-// compiler does not count these loads (they have no destination register);
-// wait_loads does.  Nothing else in these kernels uses m0.
-__device__ __forceinline__ void load_to_lds(i32x4 view, uint32_t offset, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               :
-               : "s"(lds), "v"(offset), "s"(view)
-               : "memory");
-}
-
-// Until no more than N of the wave's loads are outstanding.
-template <int N> __device__ __forceinline__ void wait_loads() {
-  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
-}
-
-__device__ __forceinline__ void barrier() {
-  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory");
-}
-
-__device__ __forceinline__ i32x4 buffer_view(const uint8_t *base, uint32_t bytes) {
-  const uint64_t a = reinterpret_cast<uint64_t>(base);
-  return i32x4{__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
-               __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32) & 0xFFFF),
-               __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
-}
-
-// Scale bytes of 16 consecutive blocks of a row at any alignment; blocks past
-// the row's end read as 127.
-struct __attribute__((packed)) Packed16 { uint32_t v[4]; };
-__device__ __forceinline__ u32x4 load_scales16(const uint8_t *row, int64_t block, int64_t nb) {
-  u32x4 r;
-  if (block + 16 <= nb) {
-    const Packed16 p = *reinterpret_cast<const Packed16 *>(row + block);
-    r = u32x4{p.v[0], p.v[1], p.v[2], p.v[3]};
-  } else {
-    for (int i = 0; i < 4; i++) {
-      uint32_t v = 0;
-      for (int j = 0; j < 4; j++)
-        v |= (uint32_t)(block + 4 * i + j < nb ? row[block + 4 * i + j] : 127) << (8 * j);
-      r[i] = v;
-    }
-  }
-  return r;
-}
-
-// r[j] holds blocks 4j .. 4j+3 of step j; afterwards dword g holds block g of
-// the four steps, one to a byte.
-__device__ __forceinline__ u32x4 transpose_bytes(u32x4 r) {
-  const uint32_t a = __builtin_amdgcn_perm(r[1], r[0], 0x05010400);  // 0.0 1.0 0.1 1.1
-  const uint32_t b = __builtin_amdgcn_perm(r[1], r[0], 0x07030602);  // 0.2 1.2 0.3 1.3
-  const uint32_t c = __builtin_amdgcn_perm(r[3], r[2], 0x05010400);
-  const uint32_t d = __builtin_amdgcn_perm(r[3], r[2], 0x07030602);
-  return u32x4{__builtin_amdgcn_perm(c, a, 0x05040100), __builtin_amdgcn_perm(c, a, 0x07060302),
-               __builtin_amdgcn_perm(d, b, 0x05040100), __builtin_amdgcn_perm(d, b, 0x07060302)};
-}
-
 // BM tokens x BN weight rows per workgroup of WM x WN waves, each with
-// TM x TN tiles of 16x16.
-template <int AF, int T, int WM, int WN, int TM, int TN>
-__global__ __launch_bounds__(kThreads, 2) void mxfp4_tiled_kernel(
+// TM x TN tiles of 16x16; S stages of KS 128-position steps in LDS.  ALIGNED:
+// rows of whole steps whose scales start at dwords.
+template <int AF, int T, int WM, int WN, int TM, int TN, int KS, int S, bool ALIGNED>
+__global__ __launch_bounds__(64 * WM * WN, 2) void mxfp4_tiled_kernel(
     const uint8_t *a, const uint8_t *as, const uint8_t *w, const uint8_t *ws, void *y, int M,
     int64_t K, int64_t N, int tiles_m, int tiles_n) {
+  constexpr int kW = WM * WN, kThreads = 64 * kW;
+  constexpr bool kHalves = kW == 8;
   constexpr int BM = 16 * WM * TM, BN = 16 * WN * TN;
-  constexpr int AP = AF == MX_FP4 ? 1 : 2;                // 1 KiB pieces per 16 tokens
-  constexpr int kPieces = BM / 16 * AP + BN / 16;         // of a step
-  constexpr int kMine = kPieces / 8;
-  constexpr int kStage = kPieces * 1024;
-  constexpr int kScales = (BM + BN) * 16;
-  static_assert(kPieces % 8 == 0 && BM + BN <= kThreads, "");
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[kStages * kStage + 2 * kScales];
+  constexpr int AP = kTileLoads<AF>;
+  constexpr int kStepLoads = BM / 16 * AP + BN / 16;      // 1 KiB each
+  constexpr int kMine = kStepLoads / kW;
+  constexpr int kStep = kStepLoads * 1024;
+  // Scales are kept for kChunk steps at a time, 4 kChunk bytes a row.
+  constexpr int kChunk = KS == 2 ? 8 : 4;
+  constexpr int kScales = (BM + BN) * 4 * kChunk;
+  constexpr int kScaleLoads = kScales / 1024 / kW;        // of a wave
+  static_assert(kStepLoads % kW == 0 && BM % 64 == 0 && BN % 64 == 0, "whole loads");
+  static_assert(!kHalves || (KS == 1 && S == 3 && BM + BN <= kThreads), "");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[S * KS * kStep + 2 * kScales];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4;
@@ -102,61 +51,89 @@ __global__ __launch_bounds__(kThreads, 2) void mxfp4_tiled_kernel(
   const int64_t n0 = (int64_t)bn * BN;
   const int rows_m = M - m0 < BM ? M - m0 : BM, rows_n = N - n0 < BN ? (int)(N - n0) : BN;
 
-  const int64_t nb = K / 32;
-  const int steps = (int)((nb + 3) / 4);
+  const int nb = (int)(K / 32);
+  const int steps = (nb + 3) / 4;
   const uint32_t a_bytes = (uint32_t)(AF == MX_FP4 ? K / 2 : K), w_bytes = (uint32_t)(K / 2);
   const i32x4 a_view = buffer_view(a + (int64_t)m0 * a_bytes, rows_m * a_bytes);
   const i32x4 w_view = buffer_view(w + n0 * w_bytes, rows_n * w_bytes);
+  const auto token = [&](int m) { return m < rows_m ? m : rows_m - 1; };
+  const auto weight_row = [&](int n) { return n < rows_n ? n : rows_n - 1; };
 
-  // A piece is 1 KiB: 8 rows x 128 bytes (e4m3) or 16 rows x 64 (e2m1), with
-  // neighbouring lanes on neighbouring bytes of a row.  The 16-byte chunks of
-  // a row are stored in an order that changes with the row (chunk c at place
-  // c ^ spread), so that the 16 rows a fragment read takes lie on all banks.
-  // Weight rows go to the tiles in pairs: the lane that ends with rows
-  // 4g .. 4g+3 of both tiles of a pair has eight consecutive outputs.
   uint32_t offset[kMine];
-  int chunk[kMine];
 #pragma unroll
   for (int i = 0; i < kMine; i++) {
-    const int p = i * 8 + wave;
-    if (p < BM / 16 * AP) {
-      const int row = AP == 2 ? lane >> 3 : lane >> 2;
-      const int m = p * (16 / AP) + row;
-      chunk[i] = AP == 2 ? (lane & 7) ^ row : (lane & 3) ^ ((row >> 1) & 3);
-      offset[i] = (uint32_t)(m < rows_m ? m : rows_m - 1) * a_bytes + 16 * chunk[i];
-    } else {
-      const int t = p - BM / 16 * AP, row = lane >> 2;
-      const int n = (t >> 1) * 32 + (row >> 2) * 8 + (t & 1) * 4 + (row & 3);
-      chunk[i] = (lane & 3) ^ ((row >> 1) & 3);
-      offset[i] = (uint32_t)(n < rows_n ? n : rows_n - 1) * w_bytes + 16 * chunk[i];
-    }
+    const int p = i * kW + wave;
+    if (p < BM / 16 * AP)
+      offset[i] = (uint32_t)token(p * (16 / AP) + tile_row<AF>(lane)) * a_bytes +
+                  16 * tile_chunk<AF>(lane);
+    else
+      offset[i] = (uint32_t)weight_row(paired_row(p - BM / 16 * AP, tile_row<MX_FP4>(lane))) *
+                      w_bytes + 16 * tile_chunk<MX_FP4>(lane);
   }
-  // where a lane finds the chunks of its row in a 16-row tile
-  const int at_w = r * 64 + 16 * (g ^ ((r >> 1) & 3));
-  const int at_a = AP == 2 ? r * 128 + 16 * (g ^ (r & 7)) : at_w;
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void *)lds;
-  const int whole = (int)(nb / 4);  // steps of four blocks
-  const auto issue = [&](int s, int buf) {
-    const int blocks = (int)(nb - 4 * (int64_t)s);
+  const uint32_t lds0 = lds_address(lds);
+  // The loads of stage u: its KS steps, zeros past the row's end.
+  const auto issue = [&](int u, int buf) {
 #pragma unroll
-    for (int i = 0; i < kMine; i++) {
-      const int p = i * 8 + wave;
-      const bool is_a = p < BM / 16 * AP;
-      uint32_t o = offset[i] + (uint32_t)s * (is_a ? 64 * AP : 64);
-      if (s >= whole) {  // the row's last blocks: zeros after them
-        const int block = is_a && AP == 2 ? chunk[i] >> 1 : chunk[i];
-        if (block >= blocks) o = 0x7FFFFFF0u;
+    for (int k = 0; k < KS; k++) {
+      const int s = u * KS + k;
+#pragma unroll
+      for (int i = 0; i < kMine; i++) {
+        const int p = i * kW + wave;
+        const bool is_a = p < BM / 16 * AP;
+        uint32_t o = offset[i] + (uint32_t)s * (is_a ? 64 * AP : 64);
+        if (KS > 1 || 4 * s + 4 > nb) {
+          const int block = is_a ? chunk_block<AF>(tile_chunk<AF>(lane)) : tile_chunk<MX_FP4>(lane);
+          if (4 * s + block >= nb) o = kPastEnd;
+        }
+        load16_to_lds(is_a ? a_view : w_view, o, lds0 + (buf * KS + k) * kStep + p * 1024);
       }
-      load_to_lds(is_a ? a_view : w_view, o, lds0 + buf * kStage + p * 1024);
     }
   };
 
-  // Scales of four steps at a time, one row (token or weight) per thread.
-  const bool has_row = tid < BM + BN;
-  const uint8_t *scale_row;
-  if (tid < BM) scale_row = as + (int64_t)(m0 + (tid < rows_m ? tid : rows_m - 1)) * nb;
-  else scale_row = ws + (n0 + (tid - BM < rows_n ? tid - BM : rows_n - 1)) * nb;
-  uint8_t *const scales = lds + kStages * kStage;
+  // Scales: `row` counts the tile's tokens, then its weight rows.
+  uint8_t *const scales = lds + S * KS * kStep;
+  const auto scale_row = [&](int row) {
+    return row < BM ? as + (int64_t)(m0 + token(row)) * nb
+                    : ws + (n0 + weight_row(row - BM)) * nb;
+  };
+  // From step s on, through registers into one of the two halves: 16 bytes of
+  // a row a thread, at any alignment.
+  constexpr int kParts = kChunk / 4;                      // of a row
+  constexpr int kHold = (BM + BN) * kParts / kThreads > 0 ? (BM + BN) * kParts / kThreads : 1;
+  u32x4 held[kHold];
+  const auto load_scales = [&](int s) {
+#pragma unroll
+    for (int i = 0; i < kHold; i++) {
+      const int part = tid + i * kThreads;
+      if (part < (BM + BN) * kParts)
+        held[i] = load_scales16(scale_row(part / kParts), 4 * (int64_t)s + part % kParts * 16, nb);
+    }
+  };
+  const auto store_scales = [&](int half) {
+#pragma unroll
+    for (int i = 0; i < kHold; i++) {
+      const int part = tid + i * kThreads;
+      if (part < (BM + BN) * kParts)
+        *reinterpret_cast<u32x4 *>(scales + half * kScales + part * 16) =
+            kHalves ? transpose_bytes(held[i]) : held[i];
+    }
+  };
+  // The same straight into LDS, for rows whose scales start at dwords.
+  const i32x4 as_view = buffer_view(as + (int64_t)m0 * nb, rows_m * nb);
+  const i32x4 ws_view = buffer_view(ws + n0 * nb, rows_n * nb);
+  const auto issue_scales = [&](int s, int half) {
+    constexpr int kRows = 64 / kParts;                    // of a load
+#pragma unroll
+    for (int i = 0; i < kScaleLoads; i++) {
+      const int p = i * kW + wave;
+      const bool is_a = p < BM / kRows;
+      const int row = p * kRows + lane / kParts;
+      const uint32_t o = (uint32_t)(is_a ? token(row) : weight_row(row - BM)) * nb + 4 * s +
+                         lane % kParts * 16;
+      load16_to_lds(is_a ? as_view : ws_view, o,
+                    lds0 + S * KS * kStep + half * kScales + p * 1024);
+    }
+  };
 
   const int wm = wave % WM, wn = wave / WM;
   f32x4 acc[TM][TN];
@@ -164,102 +141,145 @@ __global__ __launch_bounds__(kThreads, 2) void mxfp4_tiled_kernel(
   for (int i = 0; i < TM; i++)
 #pragma unroll
     for (int j = 0; j < TN; j++) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-  u32x4 next = {0, 0, 0, 0};
-  if (has_row) {
-    next = load_scales16(scale_row, 0, nb);
-    *reinterpret_cast<u32x4 *>(scales + tid * 16) = transpose_bytes(next);
-  }
-  issue(0, 0);
-  if (steps > 1) {
-    issue(1, 1);
-    wait_loads<kMine>();
-  } else {
-    wait_loads<0>();
-  }
-  barrier();
-
-  // Each SIMD holds one wave of the first four and one of the others, and the
-  // second four run one barrier behind: while one wave of a SIMD multiplies a
-  // step, the other fetches its operands from LDS and sends the loads of two
-  // steps on.  A stage is overwritten after both halves have fetched from it,
-  // and read after the barrier that follows every wave's wait for it.
-  const bool behind = wave >= 4;
-  if (behind) barrier();
-  int buf = 0;
   int sa[TM], sw[TN];
-  const auto step = [&](int s, auto jc) {
-    constexpr int J = decltype(jc)::value;
-    if constexpr (J == 3) {  // read two barriers on, by both halves
-      if (has_row && s + 1 < steps)
-        *reinterpret_cast<u32x4 *>(scales + (((s >> 2) + 1) & 1) * kScales + tid * 16) =
-            transpose_bytes(next);
-    }
-    const uint8_t *st = lds + buf * kStage;
-    i32x8 ta[TM];
-    i32x4 tw[TN];
+  typedef Operand<AF> Tokens[TM];
+  typedef Operand<MX_FP4> Weights[TN];
+  const auto fetch = [&](const uint8_t *st, Tokens &ta, Weights &tw) {
 #pragma unroll
-    for (int i = 0; i < TM; i++) {
-      const uint8_t *p = st + (wm * TM + i) * AP * 1024;
-      const i32x4 lo = *reinterpret_cast<const i32x4 *>(p + at_a);
-      i32x4 hi = {0, 0, 0, 0};
-      if constexpr (AP == 2) hi = *reinterpret_cast<const i32x4 *>(p + (at_a ^ 64));
-      ta[i] = i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-    }
+    for (int i = 0; i < TM; i++)
+      ta[i] = read_operand<AF>(st + (wm * TM + i) * AP * 1024, operand_at<AF>(r, g));
 #pragma unroll
     for (int j = 0; j < TN; j++)
-      tw[j] = *reinterpret_cast<const i32x4 *>(st + (BM / 16 * AP + wn * TN + j) * 1024 + at_w);
-    if constexpr (J == 0) {
-      const uint8_t *sc = scales + ((s >> 2) & 1) * kScales;
-#pragma unroll
-      for (int i = 0; i < TM; i++)
-        sa[i] = *reinterpret_cast<const int *>(sc + ((wm * TM + i) * 16 + r) * 16 + 4 * g);
-#pragma unroll
-      for (int j = 0; j < TN; j++) {
-        const int t = wn * TN + j;
-        const int n = (t >> 1) * 32 + (r >> 2) * 8 + (t & 1) * 4 + (r & 3);
-        sw[j] = *reinterpret_cast<const int *>(sc + (BM + n) * 16 + 4 * g);
-      }
-      if (has_row && s + 4 < steps) next = load_scales16(scale_row, 4 * (int64_t)(s + 4), nb);
-    }
-    if (s + 2 < steps) {
-      issue(s + 2, buf == 0 ? 2 : buf - 1);
-      wait_loads<kMine>();
-    } else {
-      wait_loads<0>();
-    }
-    barrier();
-    __builtin_amdgcn_sched_barrier(0);
-    const auto multiply = [&](int i, int j) {
-      const i32x8 v = {tw[j][0], tw[j][1], tw[j][2], tw[j][3], 0, 0, 0, 0};
-      acc[i][j] = mfma_mx<MX_FP4, AF, T == MX_F32, J>(v, ta[i], acc[i][j], sw[j], sa[i]);
+      tw[j] = read_operand<MX_FP4>(st + (BM / 16 * AP + wn * TN + j) * 1024,
+                                   operand_at<MX_FP4>(r, g));
+  };
+  // The scales of steps s .. s+3 (a multiple of four), one to a byte; kHalves,
+  // which has no registers for four dwords a tile, keeps them so.
+  const auto fetch_scales = [&](int s) {
+    const uint8_t *sc = scales + (s / kChunk % 2) * kScales + s % kChunk * 4;
+    const uint32_t which = byte_of_two(g);
+    const auto one = [&](int row) {
+      const uint8_t *p = sc + row * 4 * kChunk;
+      if constexpr (kHalves) return *reinterpret_cast<const int *>(p + 4 * g);
+      else return (int)byte_of_four(*reinterpret_cast<const u32x4 *>(p), which);
     };
+#pragma unroll
+    for (int i = 0; i < TM; i++) sa[i] = one((wm * TM + i) * 16 + r);
+#pragma unroll
+    for (int j = 0; j < TN; j++) sw[j] = one(BM + paired_row(wn * TN + j, r));
+  };
+  const auto multiply = [&](const Tokens &ta, const Weights &tw, auto jc) {
+    constexpr int J = decltype(jc)::value;
     if constexpr (T == MX_F32 && AF == MX_FP8) {  // tokens outside: each is split in two once
 #pragma unroll
       for (int i = 0; i < TM; i++)
 #pragma unroll
-        for (int j = 0; j < TN; j++) multiply(i, j);
+        for (int j = 0; j < TN; j++)
+          acc[i][j] = mfma_mx<MX_FP4, AF, true, J>(eight(tw[j]), eight(ta[i]), acc[i][j], sw[j],
+                                                   sa[i]);
     } else {
 #pragma unroll
       for (int j = 0; j < TN; j++)
 #pragma unroll
-        for (int i = 0; i < TM; i++) multiply(i, j);
+        for (int i = 0; i < TM; i++)
+          acc[i][j] = mfma_mx<MX_FP4, AF, false, J>(eight(tw[j]), eight(ta[i]), acc[i][j], sw[j],
+                                                    sa[i]);
     }
-    __builtin_amdgcn_sched_barrier(0);
-    barrier();
-    __builtin_amdgcn_sched_barrier(0);
-    buf = buf == 2 ? 0 : buf + 1;
   };
-  for (int s = 0; s < steps; s += 4) {
-    step(s, std::integral_constant<int, 0>{});
-    if (s + 1 < steps) step(s + 1, std::integral_constant<int, 1>{});
-    if (s + 2 < steps) step(s + 2, std::integral_constant<int, 2>{});
-    if (s + 3 < steps) step(s + 3, std::integral_constant<int, 3>{});
-  }
-  if (!behind) barrier();
 
-  typedef typename MxStore<T>::type Out;
-  Out *const yo = static_cast<Out *>(y);
+  const int stages = (steps + KS - 1) / KS;
+  if (!ALIGNED || kHalves) {
+    load_scales(0);
+    store_scales(0);
+  } else {
+    issue_scales(0, 0);
+  }
+#pragma unroll
+  for (int u = 0; u < S - 1; u++)
+    if (u < stages) issue(u, u);
+  int buf = 0;
+  if constexpr (kHalves) {
+    // Each SIMD holds one wave of the first four and one of the others, and
+    // the second four run one barrier behind: while one wave of a SIMD
+    // multiplies a step, the other fetches its operands from LDS and sends
+    // the loads of two steps on.  A stage is overwritten after both halves
+    // have fetched from it, and read after the barrier that follows every
+    // wave's wait for it.
+    if (steps > 1) wait_loads<kMine>();
+    else wait_loads<0>();
+    lds_barrier();
+    const bool behind = wave >= 4;
+    if (behind) lds_barrier();
+    const auto step = [&](int s, auto jc) {
+      constexpr int J = decltype(jc)::value;
+      if (J == 3 && s + 1 < steps) store_scales(((s >> 2) + 1) & 1);  // read two barriers on
+      Tokens ta;
+      Weights tw;
+      fetch(lds + buf * kStep, ta, tw);
+      if constexpr (J == 0) {
+        fetch_scales(s);
+        if (s + 4 < steps) load_scales(s + 4);
+      }
+      if (s + 2 < steps) {
+        issue(s + 2, buf == 0 ? 2 : buf - 1);
+        wait_loads<kMine>();
+      } else {
+        wait_loads<0>();
+      }
+      lds_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(ta, tw, jc);
+      __builtin_amdgcn_sched_barrier(0);
+      lds_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      buf = buf == 2 ? 0 : buf + 1;
+    };
+    for (int s = 0; s < steps; s += 4) {
+      step(s, std::integral_constant<int, 0>{});
+      if (s + 1 < steps) step(s + 1, std::integral_constant<int, 1>{});
+      if (s + 2 < steps) step(s + 2, std::integral_constant<int, 2>{});
+      if (s + 3 < steps) step(s + 3, std::integral_constant<int, 3>{});
+    }
+    if (!behind) lds_barrier();
+  } else {
+    // Four steps a turn, in 4 / KS stages.  The next chunk of scales is sent
+    // for at a chunk's first stage, before the loads of a stage that is waited
+    // for within the chunk.
+    static_assert(S - 1 <= kChunk / KS && 4 % KS == 0, "");
+    const auto stage = [&](int u, auto jc) {
+      constexpr int J = decltype(jc)::value;
+      const int s = u * KS;
+      const bool chunk = J == 0 && s % kChunk == 0 && s + kChunk < steps;
+      if (u + S - 2 < stages) wait_loads<(S - 2) * kMine * KS>();
+      else wait_loads<0>();
+      lds_barrier();
+      if (chunk) {
+        if constexpr (ALIGNED) issue_scales(s + kChunk, (s / kChunk + 1) % 2);
+        else load_scales(s + kChunk);
+      }
+      if (u + S - 1 < stages) issue(u + S - 1, buf == 0 ? S - 1 : buf - 1);
+      if constexpr (J == 0) fetch_scales(s);
+      Tokens ta[KS];
+      Weights tw[KS];
+#pragma unroll
+      for (int k = 0; k < KS; k++) fetch(lds + (buf * KS + k) * kStep, ta[k], tw[k]);
+      multiply(ta[0], tw[0], jc);
+      if constexpr (KS == 2) multiply(ta[1], tw[1], std::integral_constant<int, J + 1>{});
+      if (!ALIGNED && chunk) store_scales((s / kChunk + 1) % 2);
+      buf = buf == S - 1 ? 0 : buf + 1;
+    };
+    for (int u = 0; u < stages; u += 4 / KS) {
+      stage(u, std::integral_constant<int, 0>{});
+      if constexpr (KS == 2) {
+        if (u + 1 < stages) stage(u + 1, std::integral_constant<int, 2>{});
+      } else {
+        if (u + 1 < stages) stage(u + 1, std::integral_constant<int, 1>{});
+        if (u + 2 < stages) stage(u + 2, std::integral_constant<int, 2>{});
+        if (u + 3 < stages) stage(u + 3, std::integral_constant<int, 3>{});
+      }
+    }
+  }
+
   const bool wide = N % 8 == 0 && (reinterpret_cast<uintptr_t>(y) & 15) == 0;
 #pragma unroll
   for (int i = 0; i < TM; i++) {
@@ -268,31 +288,48 @@ __global__ __launch_bounds__(kThreads, 2) void mxfp4_tiled_kernel(
 #pragma unroll
     for (int j = 0; j < TN; j += 2) {
       const int n = (wn * TN + j) * 16 + 8 * g;
-      const int64_t at = (int64_t)(m0 + m) * N + n0 + n;
       float f[8];
 #pragma unroll
       for (int q = 0; q < 4; q++) {
         f[q] = acc[i][j][q];
         f[4 + q] = acc[i][j + 1][q];
       }
-      if (wide && n + 8 <= rows_n) {
-        store_raw8<T>(yo + at, 0, f32_to_raw8<T>(f));
-      } else {
-#pragma unroll
-        for (int q = 0; q < 8; q++)
-          if (n + q < rows_n) yo[at + q] = (Out)f[q];
-      }
+      store_row8<T>(y, (int64_t)(m0 + m) * N + n0 + n, f, rows_n - n, wide);
     }
   }
 }
 
-template <int AF, int T, int WM, int WN, int TM, int TN>
+template <int AF, int T, int WM, int WN, int TM, int TN, int KS, int S, bool ALIGNED>
 void launch(const uint8_t *a, const uint8_t *as, const uint8_t *w, const uint8_t *ws, int M,
             int64_t K, int64_t N, void *Y, hipStream_t stream) {
   const int tm = (M + 16 * WM * TM - 1) / (16 * WM * TM);
   const int tn = (int)((N + 16 * WN * TN - 1) / (16 * WN * TN));
-  hipLaunchKernelGGL((mxfp4_tiled_kernel<AF, T, WM, WN, TM, TN>), dim3(tm * tn), dim3(kThreads), 0,
-                     stream, a, as, w, ws, Y, M, K, N, tm, tn);
+  hipLaunchKernelGGL((mxfp4_tiled_kernel<AF, T, WM, WN, TM, TN, KS, S, ALIGNED>), dim3(tm * tn),
+                     dim3(64 * WM * WN), 0, stream, a, as, w, ws, Y, M, K, N, tm, tn);
+}
+
+// The tile by estimated time.  Measured at input_dim 4096, e4m3 tokens, bf16
+// outputs (graph replays, us): 64x64 tiles 11.5 up to 256 of them, 18.2 for
+// 512, 31 for 1024, 56.6 for 2048; 128x128 tiles 23.4 for 128, 25.0 for 256,
+// 39.3 for 512, 68 for 896; 256x256 tiles 44.6 for 64, 51.7 for 224, 200 for
+// 896, a whole round of 256 at a time.  Other lengths scale all three alike.
+template <int AF, int T>
+void choose(const uint8_t *a, const uint8_t *as, const uint8_t *w, const uint8_t *ws, int M,
+            int64_t K, int64_t N, void *Y, hipStream_t stream) {
+  const auto tiles = [&](int b) { return (double)((M + b - 1) / b) * (double)((N + b - 1) / b); };
+  const double small = std::max(11.0, 5.0 + 0.0255 * tiles(64));
+  const double middle = std::max(23.0, 7.0 + 0.068 * tiles(128));
+  const double large = 50.0 * std::ceil(tiles(256) / 256.0);
+  const bool aligned = mx_aligned_scales(as, ws, K);
+  if (large <= middle && large <= small) {
+    launch<AF, T, 4, 2, 4, 8, 1, 3, true>(a, as, w, ws, M, K, N, Y, stream);
+  } else if (middle <= small) {
+    if (aligned) launch<AF, T, 2, 2, 4, 4, 1, 3, true>(a, as, w, ws, M, K, N, Y, stream);
+    else launch<AF, T, 2, 2, 4, 4, 1, 3, false>(a, as, w, ws, M, K, N, Y, stream);
+  } else {
+    if (aligned) launch<AF, T, 2, 2, 2, 2, 2, 3, true>(a, as, w, ws, M, K, N, Y, stream);
+    else launch<AF, T, 2, 2, 2, 2, 2, 3, false>(a, as, w, ws, M, K, N, Y, stream);
+  }
 }
 
 }  // namespace
@@ -300,11 +337,11 @@ void launch(const uint8_t *a, const uint8_t *as, const uint8_t *w, const uint8_t
 hipError_t mxfp4_matmul_tiled_launch(const uint8_t *a, const uint8_t *as, int a_format,
                                      const uint8_t *w, const uint8_t *ws, int64_t M, int64_t K,
                                      int64_t N, void *Y, int type, hipStream_t stream) {
-#define CALL(AF)                                                                                  \
-  switch (type) {                                                                                 \
-    case MX_F32: launch<AF, MX_F32, 4, 2, 4, 8>(a, as, w, ws, (int)M, K, N, Y, stream); break;    \
-    case MX_BF16: launch<AF, MX_BF16, 4, 2, 4, 8>(a, as, w, ws, (int)M, K, N, Y, stream); break;  \
-    default: launch<AF, MX_F16, 4, 2, 4, 8>(a, as, w, ws, (int)M, K, N, Y, stream); break;        \
+#define CALL(AF)                                                                         \
+  switch (type) {                                                                        \
+    case MX_F32: choose<AF, MX_F32>(a, as, w, ws, (int)M, K, N, Y, stream); break;       \
+    case MX_BF16: choose<AF, MX_BF16>(a, as, w, ws, (int)M, K, N, Y, stream); break;     \
+    default: choose<AF, MX_F16>(a, as, w, ws, (int)M, K, N, Y, stream); break;           \
   }
   if (a_format == MX_FP4) { CALL(MX_FP4) } else { CALL(MX_FP8) }
 #undef CALL
