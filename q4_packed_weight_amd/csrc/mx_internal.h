@@ -28,11 +28,15 @@ hipError_t mxfp4_matmul_tiled_launch(const uint8_t *a, const uint8_t *as, int a_
                                      int64_t N, void *Y, int type, hipStream_t stream);
 
 // The mixture-of-experts layer works on at most kMoeTokens tokens at a time,
-// and on no more than keep its logits in 32 KiB of LDS.
+// on no more than keep its logits in 32 KiB of LDS, and on no more than keep
+// the parts of x and h within the 31 bits of a buffer view's offsets.
 constexpr int kMoeTokens = 64;
 constexpr int kMoeMaxLogits = 8192;
-inline int64_t moe_tokens_at_once(int64_t E) {
-  return kMoeMaxLogits / E < kMoeTokens ? kMoeMaxLogits / E : kMoeTokens;
+inline int64_t moe_tokens_at_once(int64_t H, int64_t F, int64_t E, int64_t k) {
+  const int64_t by_logits = kMoeMaxLogits / E, widest = H > k * F ? H : k * F;
+  const int64_t by_view = (((int64_t)1 << 31) - 4096) / (6 * widest);
+  const int64_t n = by_logits < by_view ? by_logits : by_view;
+  return n < kMoeTokens ? n : kMoeTokens;
 }
 constexpr int kMoeMaxExperts = 256;
 constexpr int kMoeMaxTopK = 16;
@@ -43,7 +47,7 @@ struct MoeArgs {
   const uint8_t *up, *up_s, *down, *down_s;
   void *y;
   void *workspace;
-  int type, T, H, F, E, k;  // T <= moe_tokens_at_once(E)
+  int type, T, H, F, E, k;  // T <= moe_tokens_at_once(H, F, E, k)
 };
 int64_t moe_workspace_bytes(int64_t T, int64_t H, int64_t F, int64_t E, int64_t k);
 hipError_t mxfp4_moe_launch(const MoeArgs &a, hipStream_t stream);

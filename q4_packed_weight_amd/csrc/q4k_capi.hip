@@ -635,7 +635,7 @@ int mxfp4_moe(const void *x, int type, const void *router, const float *router_b
              "mxfp4_moe: the scratch workspace is smaller than mxfp4_moe_workspace_size");
     return Q4K_ESCRATCH;
   }
-  const int64_t most = q4k::moe_tokens_at_once(n_experts);
+  const int64_t most = q4k::moe_tokens_at_once(input_dim, ffn_dim, n_experts, top_k);
   const int64_t row_bytes = input_dim * (type == MX_F32 ? 4 : 2);
   for (int64_t t = 0; t < n_tokens; t += most) {
     const int64_t n = n_tokens - t < most ? n_tokens - t : most;
