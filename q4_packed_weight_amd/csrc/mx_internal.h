@@ -29,11 +29,12 @@ hipError_t mxfp4_matmul_tiled_launch(const uint8_t *a, const uint8_t *as, int a_
 
 // The mixture-of-experts layer works on at most kMoeTokens tokens at a time,
 // on no more than keep its logits in 32 KiB of LDS, and on no more than keep
-// the parts of x and h within the 31 bits of a buffer view's offsets.
+// the parts of x and h and the slots' outputs within the 31 bits of a buffer
+// view's offsets.
 constexpr int kMoeTokens = 64;
 constexpr int kMoeMaxLogits = 8192;
 inline int64_t moe_tokens_at_once(int64_t H, int64_t F, int64_t E, int64_t k) {
-  const int64_t by_logits = kMoeMaxLogits / E, widest = H > k * F ? H : k * F;
+  const int64_t by_logits = kMoeMaxLogits / E, widest = k * (H > F ? H : F);
   const int64_t by_view = (((int64_t)1 << 31) - 4096) / (6 * widest);
   const int64_t n = by_logits < by_view ? by_logits : by_view;
   return n < kMoeTokens ? n : kMoeTokens;
