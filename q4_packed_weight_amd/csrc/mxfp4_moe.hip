@@ -32,9 +32,10 @@ template <int NP> __device__ __forceinline__ void split_bf16(float v, __bf16 (&p
   }
 }
 
-// The order of logits as unsigned integers: NaN lowest, -0 equal to +0.
+// The order of logits as unsigned integers from 1 on: NaN lowest, -0 equal
+// to +0.
 __device__ __forceinline__ uint32_t logit_key(float l) {
-  if (l != l) return 0u;
+  if (l != l) return 1u;
   const uint32_t b = __builtin_bit_cast(uint32_t, l + 0.0f);
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
@@ -42,9 +43,8 @@ __device__ __forceinline__ uint32_t logit_key(float l) {
 // Workspace of up to kMoeTokens tokens.
 struct Workspace {
   float *logits;        // [T][E]
-  int *count;           // [E] tokens of an expert (of a reached one at least)
-  int *slots;           // [E][kMoeTokens] their slots: token * k + rank
-  int *chosen;          // [T*k] expert of a slot
+  int *work;            // [groups] an expert and its number of tokens << 16
+  int *slots;           // [groups][kMoeTokens] their slots: token * k + rank
   float *chosen_logit;  // [T*k]
   unsigned *arrived;    // [H/16] workgroups of the down product that are done
   __bf16 *xp;           // [NPX][T][H] x in bf16 parts, none for bf16 x
@@ -71,9 +71,8 @@ Workspace layout(void *base, int type, int64_t T, int64_t H, int64_t F, int64_t 
     return at;
   };
   w.logits = reinterpret_cast<float *>(take(T * E * 4));
-  w.count = reinterpret_cast<int *>(take(E * 4));
+  w.work = reinterpret_cast<int *>(take(E * 4));
   w.slots = reinterpret_cast<int *>(take(E * kMoeTokens * 4));
-  w.chosen = reinterpret_cast<int *>(take(T * k * 4));
   w.chosen_logit = reinterpret_cast<float *>(take(T * k * 4));
   w.arrived = reinterpret_cast<unsigned *>(take(H / 16 * 4));
   w.xp = reinterpret_cast<__bf16 *>(take(px * T * H * 2));
@@ -161,16 +160,16 @@ __device__ __forceinline__ void decode_block(i32x4 c, uint32_t s, bf16x8 (&a)[4]
 }
 
 // What a workgroup's waves multiply: V views of NRV tiles of 16 weight rows
-// each, and 16 columns of activations in NP bf16 parts.
+// each, and 4 XC columns of activations in NP bf16 parts.
 template <int V, int NRV> struct Rows {
   i32x4 codes[V], scales[V];      // views of the tiles' rows
   const uint8_t *scale_base[V];
   uint32_t code_at[V * NRV];      // this lane's bytes of its row of a load
   uint32_t scale_at[V];           // this lane's row (tile lane / 16, row lane % 16)
 };
-struct Columns {
+template <int XC> struct Columns {  // 4 XC of them
   i32x4 view;
-  uint32_t at[4], part_bytes;     // this lane's bytes of its row of each load
+  uint32_t at[XC], part_bytes;    // this lane's bytes of its row of each load
 };
 
 // The rows n0 .. n0+16 NRV-1 (the last one again past `rows`) of a matrix.
@@ -190,15 +189,15 @@ __device__ __forceinline__ void set_rows(Rows<V, NRV> &w, int v, const uint8_t *
   w.scale_at[v] = row(lane) * nb;
 }
 
-// 16 columns: `source(i)` is the row of the activations [..][K] of column i,
+// The columns: `source(i)` is the row of the activations [..][K] of column i,
 // negative for none.  A step's 128 positions of a column are 256 bytes, in 16
 // chunks of eight values; chunk c is kept at place c ^ (column % 8), so that
 // an operand read of eight columns lies on all banks.
-template <class F>
-__device__ __forceinline__ void set_columns(Columns &x, F source, int64_t K) {
+template <int XC, class F>
+__device__ __forceinline__ void set_columns(Columns<XC> &x, F source, int64_t K) {
   const int lane = threadIdx.x & 63;
 #pragma unroll
-  for (int i = 0; i < 4; i++) {
+  for (int i = 0; i < XC; i++) {
     const int column = 4 * i + (lane >> 4), chunk = (lane & 15) ^ (column & 7);
     const int row = source(column);
     x.at[i] = row < 0 ? kPastEnd : (uint32_t)row * (uint32_t)(2 * K) + 16 * chunk;
@@ -209,37 +208,42 @@ __device__ __forceinline__ void set_columns(Columns &x, F source, int64_t K) {
 // stages of its own in LDS at `ring` (no barrier), the scales of four steps
 // behind them.  ALIGNED: rows of whole steps whose scales start at dwords;
 // others come through registers, whose wait also waits for what is in flight.
-template <int V, int NRV, int NP, int S, bool ALIGNED> struct MoeRing {
-  static constexpr int kTiles = V * NRV, kLoads = kTiles + 4 * NP;
+template <int V, int NRV, int XC, int NP, int S, bool ALIGNED> struct MoeRing {
+  static constexpr int kTiles = V * NRV, kLoads = kTiles + XC * NP;
   static constexpr int kBytes = (S * kLoads + V) * 1024;
-  static_assert(S >= 2 && S <= 4 && NRV <= 4, "");
+  static_assert((S == 2 || S == 3) && NRV <= 4, "");
 };
-template <int V, int NRV, int NP, int S, bool ALIGNED>
-__device__ __forceinline__ void moe_stream(uint8_t *ring, const Rows<V, NRV> &w, const Columns &x,
-                                           int nb, int first, int last, f32x4 (&acc)[V * NRV]) {
-  typedef MoeRing<V, NRV, NP, S, ALIGNED> R;
+// The first stages' weights are sent for before `columns(x)` says where the
+// activations are, or that there are none (false, which is the result then).
+template <int V, int NRV, int XC, int NP, int S, bool ALIGNED, class F>
+__device__ __forceinline__ bool moe_stream(uint8_t *ring, const Rows<V, NRV> &w, Columns<XC> &x,
+                                           F columns, int nb, int first, int last,
+                                           f32x4 (&acc)[V * NRV]) {
+  typedef MoeRing<V, NRV, XC, NP, S, ALIGNED> R;
   constexpr int kLoads = R::kLoads;
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const uint32_t to_ring = lds_address(ring);
   uint8_t *const scales = ring + S * kLoads * 1024;
 #pragma unroll
   for (int i = 0; i < R::kTiles; i++) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  if (first >= last) return;
-  const auto issue = [&](int s, int buf) {
+  const auto issue_w = [&](int s, int buf) {
     const uint32_t to = to_ring + buf * (kLoads * 1024);
     const bool in_w = ALIGNED || 4 * s + tile_chunk<MX_FP4>(lane) < nb;
 #pragma unroll
     for (int i = 0; i < R::kTiles; i++)
       load16_to_lds(w.codes[i / NRV], in_w ? w.code_at[i] + 64u * s : kPastEnd,
-                    to + (4 * NP + i) * 1024);
+                    to + (XC * NP + i) * 1024);
+  };
+  const auto issue_x = [&](int s, int buf) {
+    const uint32_t to = to_ring + buf * (kLoads * 1024);
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
+    for (int i = 0; i < XC; i++) {
       const int chunk = (lane & 15) ^ ((4 * i + (lane >> 4)) & 7);
       const bool in_x = ALIGNED || 4 * s + (chunk >> 2) < nb;
 #pragma unroll
       for (int q = 0; q < NP; q++)
         load16_to_lds(x.view, in_x ? x.at[i] + q * x.part_bytes + 256u * s : kPastEnd,
-                      to + (4 * q + i) * 1024);
+                      to + (XC * q + i) * 1024);
     }
   };
   u32x4 held[V];
@@ -254,30 +258,52 @@ __device__ __forceinline__ void moe_stream(uint8_t *ring, const Rows<V, NRV> &w,
       load16_to_lds(w.scales[v], lane < 16 * NRV ? w.scale_at[v] + 4u * s : kPastEnd,
                     to_ring + (S * kLoads + v) * 1024);
   };
-  if constexpr (ALIGNED) issue_scales(first);
-  else load_scales(first);
+  if (first < last) {
+    if constexpr (ALIGNED) issue_scales(first);
+    else load_scales(first);
+  }
 #pragma unroll
   for (int d = 0; d < S - 1; d++)
-    if (first + d < last) issue(first + d, d);
+    if (first + d < last) issue_w(first + d, d);
+  if (!columns(x)) {
+    wait_loads<0>();
+    return false;
+  }
+  if (first >= last) return true;
+#pragma unroll
+  for (int d = 0; d < S - 1; d++)
+    if (first + d < last) issue_x(first + d, d);
   int buf = 0;
   uint32_t sc[R::kTiles];
-  const auto step = [&](int s, auto jc) {
-    constexpr int J = decltype(jc)::value;
-    wait_lds();  // what the next loads overwrite is read
-    if constexpr (J == 1) {
-      if (s + 3 < last) {
-        if constexpr (ALIGNED) issue_scales(s + 3);
-        else load_scales(s + 3);
-      }
+  // Not unrolled: a workgroup runs few steps, and code that is fetched for
+  // one use costs more than the loop.
+#pragma unroll 1
+  for (int s = first; s < last; s++) {
+    const int j4 = (s - first) & 3;  // of the four steps whose scales are at hand
+    wait_lds();                      // what the next loads overwrite is read
+    if (j4 == 1 && s + 3 < last) {
+      if constexpr (ALIGNED) issue_scales(s + 3);
+      else load_scales(s + 3);
     }
-    if (s + S - 1 < last) issue(s + S - 1, buf == 0 ? S - 1 : buf - 1);
-    // The scales of the steps from s on are older than stage s.
+    if (s + S - 1 < last) {
+      issue_w(s + S - 1, buf == 0 ? S - 1 : buf - 1);
+      issue_x(s + S - 1, buf == 0 ? S - 1 : buf - 1);
+    }
+    // The scales of the steps from s on are older than stage s; younger are
+    // the stages ahead, of which the second one's weights (S = 3) are older
+    // than the first one's activations.
     const int ahead = last - 1 - s;
-    if (S > 3 && ahead >= 3) wait_loads<(S > 3 ? 3 : 0) * kLoads>();
-    else if (S > 2 && ahead >= 2) wait_loads<(S > 2 ? 2 : 0) * kLoads>();
-    else if (ahead >= 1) wait_loads<kLoads>();
-    else wait_loads<0>();
-    if constexpr (J == 0) {
+    constexpr int kSecond = S == 3 ? XC * NP : kLoads;
+    if (s == first) {
+      if (S == 3 && ahead >= 2) wait_loads<kSecond + kLoads>();
+      else if (ahead >= 1) wait_loads<kSecond>();
+      else wait_loads<0>();
+    } else {
+      if (S == 3 && ahead >= 2) wait_loads<(S - 1) * kLoads>();
+      else if (ahead >= 1) wait_loads<kLoads>();
+      else wait_loads<0>();
+    }
+    if (j4 == 0) {
       if constexpr (!ALIGNED) {
 #pragma unroll
         for (int v = 0; v < V; v++)
@@ -291,18 +317,19 @@ __device__ __forceinline__ void moe_stream(uint8_t *ring, const Rows<V, NRV> &w,
                                                               i % NRV * 256 + r * 16), which);
     }
     const uint8_t *st = ring + buf * (kLoads * 1024);
+    const int column = XC == 4 ? r : r % (4 * XC);  // the others' results are not used
     bf16x8 b[NP][4];
 #pragma unroll
     for (int q = 0; q < NP; q++)
 #pragma unroll
       for (int j = 0; j < 4; j++)
-        b[q][j] = *reinterpret_cast<const bf16x8 *>(st + q * 4096 + r * 256 +
-                                                    16 * ((4 * g + j) ^ (r & 7)));
+        b[q][j] = *reinterpret_cast<const bf16x8 *>(st + q * (XC * 1024) + column * 256 +
+                                                    16 * ((4 * g + j) ^ (column & 7)));
 #pragma unroll
     for (int i = 0; i < R::kTiles; i++) {
       bf16x8 a[4];
-      decode_block(read_operand<MX_FP4>(st + (4 * NP + i) * 1024, operand_at<MX_FP4>(r, g)).v,
-                   (sc[i] >> (8 * J)) & 255u, a);
+      decode_block(read_operand<MX_FP4>(st + (XC * NP + i) * 1024, operand_at<MX_FP4>(r, g)).v,
+                   (sc[i] >> (8 * j4)) & 255u, a);
 #pragma unroll
       for (int q = 0; q < NP; q++)
 #pragma unroll
@@ -310,14 +337,9 @@ __device__ __forceinline__ void moe_stream(uint8_t *ring, const Rows<V, NRV> &w,
           acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[j], b[q][j], acc[i], 0, 0, 0);
     }
     buf = buf == S - 1 ? 0 : buf + 1;
-  };
-  for (int s = first; s < last; s += 4) {
-    step(s, std::integral_constant<int, 0>{});
-    if (s + 1 < last) step(s + 1, std::integral_constant<int, 1>{});
-    if (s + 2 < last) step(s + 2, std::integral_constant<int, 2>{});
-    if (s + 3 < last) step(s + 3, std::integral_constant<int, 3>{});
   }
   wait_lds();
+  return true;
 }
 
 // The waves' sums of tile i, in wave order, from where moe_stream's rings
@@ -340,77 +362,109 @@ struct UpArgs {
   const __bf16 *xp;
   const float *logits;
   const uint8_t *up, *up_s;
-  int *count, *slots, *chosen;
+  int *work, *slots;
   float *chosen_logit;
   __bf16 *hp;
   int T, H, F, E, k;
   int by_slot;  // blockIdx.y is a slot, else an expert
 };
 
+// The dwords from one token's keys to the next one's in LDS: whole 16 bytes,
+// and not a multiple of all banks.
+__host__ __device__ inline int key_stride(int E) { return (E + 3) / 4 * 4 + 4; }
+
+// How many of the experts from..to-1 (multiples of 4; keys past the last
+// expert are 0) come before expert q: a greater key, or the same one at a
+// lower index.  Whole quads before q's take keys of mine on, those after it
+// greater ones; only q's own quad looks at its places.
+__device__ __forceinline__ int count_before(const uint32_t *row, int from, int to, int q) {
+  const uint32_t mine = row[q];
+  const int own = q & ~3;
+  int before = 0;
+#pragma unroll 4
+  for (int i = from; i < to; i += 4) {
+    const u32x4 v = *reinterpret_cast<const u32x4 *>(row + i);
+    const uint32_t least = i < own ? mine - 1 : mine;
+#pragma unroll
+    for (int c = 0; c < 4; c++) before += v[c] > least;
+  }
+  if (own >= from && own < to) {
+    const u32x4 v = *reinterpret_cast<const u32x4 *>(row + own);
+#pragma unroll
+    for (int c = 0; c < 3; c++) before += own + c < q && v[c] == mine;
+  }
+  return before;
+}
+
 // Gate and up rows of 16 NF positions of one expert for every token that
-// chose it, 16 tokens at a time.  An expert's rank for a token is the number
+// chose it, 4 XC tokens at a time.  An expert's rank for a token is the number
 // of experts before it in the order (logit descending, index ascending), so
 // each workgroup finds its tokens by counting, without a sort; ranks below k
 // are the chosen ones and give each slot exactly one writer.
-template <int NPX, int NPH, int NF, int W, int S, bool ALIGNED>
+template <int NPX, int NPH, int NF, int XC, int W, int S, bool ALIGNED>
 __global__ __launch_bounds__(W * 64) void moe_up_kernel(UpArgs p) {
-  typedef MoeRing<2, NF, NPX, S, ALIGNED> Ring;
-  // the logits' keys [T][E] first, the waves' rings later
-  constexpr int kBytes = W * Ring::kBytes > kMoeMaxLogits * 4 ? W * Ring::kBytes : kMoeMaxLogits * 4;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[kBytes];
-  uint32_t *const keys = reinterpret_cast<uint32_t *>(lds);
+  typedef MoeRing<2, NF, XC, NPX, S, ALIGNED> Ring;
+  constexpr int kThreads = W * 64;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[W * Ring::kBytes];
+  extern __shared__ u32x4 key_lds[];  // the logits' keys [T][key_stride(E)]
+  uint32_t *const keys = reinterpret_cast<uint32_t *>(key_lds);
   __shared__ int rank_of[kMoeTokens];
   __shared__ int list[kMoeTokens];  // token | rank << 8
   __shared__ int found, list_n;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  for (int i = tid; i < p.T * p.E; i += W * 64) keys[i] = logit_key(p.logits[i]);
-  __syncthreads();
+  const int stride = key_stride(p.E), padded = stride - 4;
+  // eight tokens' logits in flight at a time
+  for (int t0 = wave; t0 < p.T; t0 += 8 * W)
+    for (int q = lane; q < padded; q += 64) {
+      float l[8];
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        const int t = t0 + j * W;
+        l[j] = t < p.T && q < p.E ? p.logits[t * p.E + q] : 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; j++)
+        if (t0 + j * W < p.T)
+          keys[(t0 + j * W) * stride + q] = q < p.E ? logit_key(l[j]) : 0u;
+    }
+  if (tid < kMoeTokens) rank_of[tid] = 0;
+  lds_barrier();
   int e = blockIdx.y, t_first = -1;
   if (p.by_slot) {
     t_first = blockIdx.y / p.k;
     const int rank = blockIdx.y % p.k;
-    for (int q = tid; q < p.E; q += W * 64) {
-      const uint32_t *row = keys + t_first * p.E;
-      const uint32_t mine = row[q];
-      int before = 0;
-      for (int i = 0; i < p.E; i++) before += row[i] > mine || (row[i] == mine && i < q);
-      if (before == rank) found = q;
-    }
-    __syncthreads();
+    const uint32_t *row = keys + t_first * stride;
+    for (int q = tid; q < p.E; q += kThreads)
+      if (count_before(row, 0, padded, q) == rank) found = q;
+    lds_barrier();
     e = __builtin_amdgcn_readfirstlane(found);
   }
-  for (int t = wave; t < p.T; t += W) {
-    const uint32_t *row = keys + t * p.E;
-    const uint32_t mine = row[e];
-    int before = 0;
-    for (int i = 0; i < p.E; i += 64) {
-      const int q = i + lane;
-      const bool b = q < p.E && (row[q] > mine || (row[q] == mine && q < e));
-      before += __popcll(__ballot(b));
+  // tokens on lanes, a wave's share of the experts each
+  const auto find_tokens = [&]() {
+    if (p.T == 1) {  // by_slot: k of E experts
+      if (tid == 0) {
+        list[0] = (int)(blockIdx.y << 8);
+        list_n = 1;
+      }
+      lds_barrier();
+      return;
     }
-    if (lane == 0) rank_of[t] = before;
-  }
-  __syncthreads();
-  if (wave == 0) {
-    const bool in = lane < p.T && rank_of[lane] < p.k;
-    const uint64_t m = __ballot(in);
-    if (in) list[__popcll(m & ((1ull << lane) - 1))] = lane | rank_of[lane] << 8;
-    if (lane == 0) list_n = __popcll(m);
-  }
-  __syncthreads();
-  const int n = __builtin_amdgcn_readfirstlane(list_n);
-  // several slots can name one expert: the first token's does its work
-  if (p.by_slot && (list[0] & 255) != t_first) return;
-  if (blockIdx.x == 0) {
-    if (tid == 0) p.count[e] = n;
-    if (tid < n) {
-      const int t = list[tid] & 255, slot = t * p.k + (list[tid] >> 8);
-      p.slots[e * kMoeTokens + tid] = slot;
-      p.chosen[slot] = e;
-      p.chosen_logit[slot] = p.logits[t * p.E + e];
+    const int from = padded / 4 * wave / W * 4, to = padded / 4 * (wave + 1) / W * 4;
+    if (lane < p.T && from < to) {
+      const uint32_t *row = keys + lane * stride;
+      atomicAdd(&rank_of[lane], count_before(row, from, to, e));
     }
-  }
+    lds_barrier();
+    if (wave == 0) {
+      const int rank = rank_of[lane];
+      const bool in = lane < p.T && rank < p.k;
+      const uint64_t m = __ballot(in);
+      if (in) list[__popcll(m & ((1ull << lane) - 1))] = lane | rank << 8;
+      if (lane == 0) list_n = __popcll(m);
+    }
+    lds_barrier();
+  };
 
   const int r = lane & 15, g = lane >> 4;
   const int f0 = blockIdx.x * (16 * NF), nb = p.H / 32, steps = (nb + 3) / 4;
@@ -420,15 +474,25 @@ __global__ __launch_bounds__(W * 64) void moe_up_kernel(UpArgs p) {
   Rows<2, NF> w;
   set_rows(w, 0, p.up + gate * (p.H / 2), p.up_s + gate * nb, rows, p.H);
   set_rows(w, 1, p.up + up * (p.H / 2), p.up_s + up * nb, rows, p.H);
-  Columns x;
+  Columns<XC> x;
   x.part_bytes = (uint32_t)p.T * p.H * 2;
   x.view = buffer_view(reinterpret_cast<const uint8_t *>(p.xp), NPX * x.part_bytes);
   uint8_t *const mine = lds + wave * Ring::kBytes;
-  for (int base = 0; base < n; base += 16) {
-    if (base) __syncthreads();
-    set_columns(x, [&](int i) { return base + i < n ? list[base + i] & 255 : -1; }, p.H);
+  int n = 0;
+  for (int base = 0; base == 0 || base < n; base += 4 * XC) {
     f32x4 acc[2 * NF];
-    moe_stream<2, NF, NPX, S, ALIGNED>(mine, w, x, nb, first, last, acc);
+    const auto columns = [&](Columns<XC> &c) {
+      if (base == 0) {
+        find_tokens();
+        n = __builtin_amdgcn_readfirstlane(list_n);
+        // several slots can name one expert: the first token's does its work
+        if (p.by_slot && (list[0] & 255) != t_first) n = 0;
+        if (n == 0) return false;
+      }
+      set_columns(c, [&](int i) { return base + i < n ? list[base + i] & 255 : -1; }, p.H);
+      return true;
+    };
+    if (!moe_stream<2, NF, XC, NPX, S, ALIGNED>(mine, w, x, columns, nb, first, last, acc)) break;
     keep_sums(mine, acc);
     __syncthreads();
     for (int i = wave; i < NF; i += W) {
@@ -442,7 +506,7 @@ __global__ __launch_bounds__(W * 64) void moe_up_kernel(UpArgs p) {
 #pragma unroll
         for (int j = 0; j < NPH; j++) part[j][c] = q[j];
       }
-      if (base + r < n && 16 * i < rows) {  // F is a multiple of 32
+      if (r < 4 * XC && base + r < n && 16 * i < rows) {  // F is a multiple of 32
         const int entry = list[base + r];
         const int64_t slot = (int64_t)(entry & 255) * p.k + (entry >> 8);
 #pragma unroll
@@ -451,40 +515,52 @@ __global__ __launch_bounds__(W * 64) void moe_up_kernel(UpArgs p) {
                                       4 * g) = part[j];
       }
     }
+    __syncthreads();  // the sums are read before the next loads overwrite them
+  }
+  if (blockIdx.x == 0) {  // for the down product
+    if (tid < n) {
+      const int t = list[tid] & 255, slot = t * p.k + (list[tid] >> 8);
+      p.slots[blockIdx.y * kMoeTokens + tid] = slot;
+      p.chosen_logit[slot] = p.logits[t * p.E + e];
+      if (p.by_slot) p.work[slot] = tid == 0 ? e | n << 16 : 0;
+    }
+    if (!p.by_slot && tid == 0) p.work[e] = e | n << 16;
   }
 }
 
 struct DownArgs {
   const __bf16 *hp;
-  const int *count, *slots, *chosen;
+  const int *work, *slots;
   const float *chosen_logit;
   const uint8_t *down, *down_s;
   float *out;
   unsigned *arrived;
   void *y;
   int T, H, F, E, k;
-  int by_slot;
 };
 
 // Output rows h0 .. h0+16 NR-1 of one expert for every token that chose it,
 // unweighted, by slot.  The workgroup that finds itself the last of its rows
 // then adds up the slots of every token, in the order of their ranks and with
 // the softmax's weights.
-template <int TY, int NR, int W, int S, bool ALIGNED>
+template <int TY, int NR, int XC, int W, int S, bool ALIGNED>
 __global__ __launch_bounds__(W * 64) void moe_down_kernel(DownArgs p) {
   constexpr int NPH = kHParts<TY>;
-  typedef MoeRing<1, NR, NPH, S, ALIGNED> Ring;
+  typedef MoeRing<1, NR, XC, NPH, S, ALIGNED> Ring;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[W * Ring::kBytes];
-  __shared__ int last_one;
+  __shared__ int slots[kMoeTokens], last_one;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const int e = __builtin_amdgcn_readfirstlane(p.by_slot ? p.chosen[blockIdx.y] : (int)blockIdx.y);
-  const int *slots = p.slots + e * kMoeTokens;
-  int n = p.count[e];
-  // several slots can name one expert: the first of its list does its work
-  if (p.by_slot && slots[0] != (int)blockIdx.y) n = 0;
-  n = __builtin_amdgcn_readfirstlane(n);
+  if (tid < kMoeTokens) slots[tid] = p.slots[blockIdx.y * kMoeTokens + tid];
+  constexpr int kHold = kMoeTokens * kMoeMaxTopK / (W * 64);
+  float chosen_logit[kHold];  // for the last workgroup, which would wait for them
+#pragma unroll
+  for (int j = 0; j < kHold; j++)
+    if (tid + j * W * 64 < p.T * p.k) chosen_logit[j] = p.chosen_logit[tid + j * W * 64];
+  const int work = __builtin_amdgcn_readfirstlane(p.work[blockIdx.y]);
+  const int e = work & 0xFFFF, n = work >> 16;
+  lds_barrier();
 
   const int h0 = blockIdx.x * (16 * NR), nb = p.F / 32, steps = (nb + 3) / 4;
   const int rows = p.H - h0 < 16 * NR ? p.H - h0 : 16 * NR;
@@ -492,21 +568,24 @@ __global__ __launch_bounds__(W * 64) void moe_down_kernel(DownArgs p) {
   const int64_t row0 = (int64_t)e * p.H + h0;
   Rows<1, NR> w;
   set_rows(w, 0, p.down + row0 * (p.F / 2), p.down_s + row0 * nb, rows, p.F);
-  Columns x;
+  Columns<XC> x;
   x.part_bytes = (uint32_t)p.T * p.k * p.F * 2;
   x.view = buffer_view(reinterpret_cast<const uint8_t *>(p.hp), NPH * x.part_bytes);
   const auto out = make_rsrc(p.out, (int64_t)p.T * p.k * p.H * 4);
   uint8_t *const mine = lds + wave * Ring::kBytes;
-  for (int base = 0; base < n; base += 16) {
+  for (int base = 0; base < n; base += 4 * XC) {
     if (base) __syncthreads();
-    set_columns(x, [&](int i) { return base + i < n ? slots[base + i] : -1; }, p.F);
     f32x4 acc[NR];
-    moe_stream<1, NR, NPH, S, ALIGNED>(mine, w, x, nb, first, last, acc);
+    const auto columns = [&](Columns<XC> &c) {
+      set_columns(c, [&](int i) { return base + i < n ? slots[base + i] : -1; }, p.F);
+      return true;
+    };
+    moe_stream<1, NR, XC, NPH, S, ALIGNED>(mine, w, x, columns, nb, first, last, acc);
     keep_sums(mine, acc);
     __syncthreads();
     for (int i = wave; i < NR; i += W) {
       const f32x4 d = sum_of<W>(lds, Ring::kBytes, i);
-      if (base + r < n && 16 * i < rows)
+      if (r < 4 * XC && base + r < n && 16 * i < rows)
         __builtin_amdgcn_raw_buffer_store_b128(
             __builtin_bit_cast(u32x4, d), out, (slots[base + r] * p.H + h0 + 16 * i + 4 * g) * 4, 0,
             kCoherent);
@@ -526,9 +605,12 @@ __global__ __launch_bounds__(W * 64) void moe_down_kernel(DownArgs p) {
                                       __HIP_MEMORY_SCOPE_AGENT) == gridDim.y - 1;
   __syncthreads();
   if (!last_one) return;
-  float *const share = reinterpret_cast<float *>(lds);  // T * k <= 1024
+  float *const logit = reinterpret_cast<float *>(lds), *const share = logit + kMoeTokens * kMoeMaxTopK;
+#pragma unroll
+  for (int j = 0; j < kHold; j++) logit[tid + j * W * 64] = chosen_logit[j];
+  __syncthreads();
   if (tid < p.T) {
-    const float *l = p.chosen_logit + tid * p.k;
+    const float *l = logit + tid * p.k;
     float sum = 0.0f;
     const float top = l[0];
     for (int i = 0; i < p.k; i++) sum += expf(l[i] - top);
@@ -536,13 +618,22 @@ __global__ __launch_bounds__(W * 64) void moe_down_kernel(DownArgs p) {
   }
   __syncthreads();
   const int quads = rows / 4;
+#pragma unroll 2
   for (int i = tid; i < p.T * quads; i += W * 64) {
     const int t = i / quads, at = h0 + i % quads * 4;
     f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int q = 0; q < p.k; q++)
-      v += share[t * p.k + q] *
-           __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                         out, ((t * p.k + q) * p.H + at) * 4, 0, kCoherent));
+    for (int q0 = 0; q0 < p.k; q0 += 4) {  // four loads in flight
+      f32x4 o[4];
+#pragma unroll
+      for (int q = 0; q < 4; q++)
+        o[q] = __builtin_bit_cast(
+            f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                       out, q0 + q < p.k ? ((t * p.k + q0 + q) * p.H + at) * 4 : (int)kPastEnd, 0,
+                       kCoherent));
+#pragma unroll
+      for (int q = 0; q < 4; q++)
+        if (q0 + q < p.k) v += share[t * p.k + q0 + q] * o[q];
+    }
 #pragma unroll
     for (int c = 0; c < 4; c++) store_value<TY>(p.y, (int64_t)t * p.H + at + c, v[c]);
   }
@@ -559,26 +650,48 @@ void launch(const MoeArgs &a, const Workspace &w, hipStream_t stream) {
                        a.x, a.router, a.bias, w.logits, w.xp, w.arrived, a.T, a.H, a.E);
   const int by_slot = a.T * a.k <= a.E, groups = by_slot ? a.T * a.k : a.E;
   const UpArgs u{TY == MX_BF16 ? static_cast<const __bf16 *>(a.x) : w.xp, w.logits, a.up, a.up_s,
-                 w.count, w.slots, w.chosen, w.chosen_logit, w.hp, a.T, a.H, a.F, a.E, a.k, by_slot};
+                 w.work, w.slots, w.chosen_logit, w.hp, a.T, a.H, a.F, a.E, a.k, by_slot};
+  const DownArgs d{w.hp, w.work, w.slots, w.chosen_logit, a.down, a.down_s, w.out, w.arrived,
+                   a.y, a.T, a.H, a.F, a.E, a.k};
   // Wide tiles read the activations less often, narrow ones make more
-  // workgroups; two workgroups' rings fit a CU's LDS.
-  constexpr int NF = NPX == 3 ? 2 : 4, SU = NPX == 1 ? 3 : 2;
+  // workgroups: the widest that make 512, two for each CU, whose rings fit the
+  // CU's LDS twice at least.
   const auto tiles = [](int rows, int n) { return (rows + 16 * n - 1) / (16 * n); };
-  if ((int64_t)tiles(a.F, NF) * groups >= 512)
-    hipLaunchKernelGGL((moe_up_kernel<NPX, NPH, NF, 2, SU, UP_ALIGNED>),
-                       dim3(tiles(a.F, NF), groups), dim3(128), 0, stream, u);
-  else
-    hipLaunchKernelGGL((moe_up_kernel<NPX, NPH, 1, 2, (NPX == 1 ? 4 : NPX == 2 ? 3 : 2), UP_ALIGNED>),
-                       dim3(tiles(a.F, 1), groups), dim3(128), 0, stream, u);
-  const DownArgs d{w.hp, w.count, w.slots, w.chosen, w.chosen_logit, a.down, a.down_s, w.out,
-                   w.arrived, a.y, a.T, a.H, a.F, a.E, a.k, by_slot};
-  constexpr int SD = NPH == 2 ? 3 : 2;
-  if ((int64_t)tiles(a.H, 4) * groups >= 512)
-    hipLaunchKernelGGL((moe_down_kernel<TY, 4, 2, SD, DOWN_ALIGNED>), dim3(tiles(a.H, 4), groups),
-                       dim3(128), 0, stream, d);
-  else
-    hipLaunchKernelGGL((moe_down_kernel<TY, 2, 2, SD, DOWN_ALIGNED>), dim3(tiles(a.H, 2), groups),
-                       dim3(128), 0, stream, d);
+  const auto run = [&](auto xc) {
+    constexpr int XC = decltype(xc)::value;
+    const auto up = [&](auto nf, auto nw, auto ns) {
+      constexpr int NF = decltype(nf)::value, W = decltype(nw)::value, S = decltype(ns)::value;
+      hipLaunchKernelGGL((moe_up_kernel<NPX, NPH, NF, XC, W, S, UP_ALIGNED>),
+                         dim3(tiles(a.F, NF), groups), dim3(64 * W),
+                         (size_t)a.T * key_stride(a.E) * 4, stream, u);
+    };
+    const auto down = [&](auto nr, auto ns) {
+      constexpr int NR = decltype(nr)::value, S = decltype(ns)::value;
+      hipLaunchKernelGGL((moe_down_kernel<TY, NR, XC, 2, S, DOWN_ALIGNED>),
+                         dim3(tiles(a.H, NR), groups), dim3(128), 0, stream, d);
+    };
+    typedef std::integral_constant<int, 1> I1;
+    typedef std::integral_constant<int, 2> I2;
+    typedef std::integral_constant<int, 4> I4;
+    // stages: three, or two where three do not fit
+    typedef std::integral_constant<int, (XC * NPX < 6 ? 3 : 2)> SX;
+    typedef std::integral_constant<int, (XC * NPH < 6 || NPH == 2 ? 3 : 2)> SH;
+    constexpr int kWide = NPX * XC < 12 ? 4 : 2;
+    if ((int64_t)tiles(a.F, kWide) * groups >= 512)
+      up(std::integral_constant<int, kWide>{}, I2{}, SX{});
+    else if ((int64_t)tiles(a.F, 2) * groups >= 512)
+      up(I2{}, I2{}, SX{});
+    else
+      up(I1{}, std::integral_constant<int, (XC == 1 ? 4 : 2)>{}, SX{});
+    if ((int64_t)tiles(a.H, 4) * groups >= 512) down(I4{}, SH{});
+    else down(I2{}, SH{});
+  };
+  // Columns at a time: all of up to four tokens; eight for up to two tokens an
+  // expert (an expert that more than eight chose takes its weights again for
+  // the next ones, as any beyond 16); 16 otherwise.
+  if (a.T <= 4) run(std::integral_constant<int, 1>{});
+  else if (a.T * a.k <= 2 * a.E) run(std::integral_constant<int, 2>{});
+  else run(std::integral_constant<int, 4>{});
 }
 
 }  // namespace
