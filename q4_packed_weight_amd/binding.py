@@ -394,36 +394,39 @@ def _mx_format(fmt):
     return code
 
 
-def _mx_codes(codes, scales, fmt, rows, K, what):
-    """Marshalling checks of a matrix in MX blocks."""
-    n = rows * K if rows > 0 and K > 0 and K % 32 == 0 else 0
-    _expect(codes, torch.uint8, f"{what}codes", n // 2 if fmt == "fp4" else n)
-    _expect(scales, torch.uint8, f"{what}scales", n // 32)
+def _arg(t, dtype, name, need):
+    """The pointer of a tensor that passes _expect's checks."""
+    if t is None:
+        return None
+    if not (t.dtype is dtype and t.is_contiguous() and t.is_cuda and t.numel() >= need):
+        _expect(t, dtype, name, need)
+    return t.data_ptr()
 
 
-def _mx_values(t, dtype, name, rows, K):
-    _expect(t, dtype, name, rows * K if rows > 0 and K > 0 else 0)
+def _mx_need(rows, K):
+    """Values of a matrix in MX blocks (0 where the C side refuses the sizes)."""
+    return rows * K if rows > 0 and K > 0 and K % 32 == 0 else 0
 
 
 def mx_quantize(x, n_rows, input_dim, fmt, codes, scales, stream=None):
     """Rows of x (fp32, bf16 or fp16) to MX blocks; fmt is "fp4" or "fp8"."""
     R, K = int(n_rows), int(input_dim)
-    t, f = _mx_type(x, "x"), _mx_format(fmt)
-    _mx_values(x, x.dtype, "x", R, K)
-    _mx_codes(codes, scales, fmt, R, K, "")
-    _check(lib().mx_quantize(_ptr(x), t, f, R, K, _ptr(codes), _ptr(scales), _stream(stream)),
-           "mx_quantize")
+    t, f, n = _mx_type(x, "x"), _mx_format(fmt), _mx_need(R, K)
+    rc = lib().mx_quantize(_arg(x, x.dtype, "x", n), t, f, R, K,
+                           _arg(codes, torch.uint8, "codes", n * f // 8),
+                           _arg(scales, torch.uint8, "scales", n // 32), _stream(stream))
+    _check(rc, "mx_quantize")
     return codes, scales
 
 
 def mx_dequantize(codes, scales, n_rows, input_dim, fmt, y, stream=None):
     """The values of MX blocks, rounded to y's type."""
     R, K = int(n_rows), int(input_dim)
-    t, f = _mx_type(y, "y"), _mx_format(fmt)
-    _mx_codes(codes, scales, fmt, R, K, "")
-    _mx_values(y, y.dtype, "y", R, K)
-    _check(lib().mx_dequantize(_ptr(codes), _ptr(scales), f, R, K, _ptr(y), t, _stream(stream)),
-           "mx_dequantize")
+    t, f, n = _mx_type(y, "y"), _mx_format(fmt), _mx_need(R, K)
+    rc = lib().mx_dequantize(_arg(codes, torch.uint8, "codes", n * f // 8),
+                             _arg(scales, torch.uint8, "scales", n // 32), f, R, K,
+                             _arg(y, y.dtype, "y", n), t, _stream(stream))
+    _check(rc, "mx_dequantize")
     return y
 
 
@@ -432,17 +435,15 @@ def mx_rmsnorm(x, residual, weight, eps, n_rows, input_dim, fmt, residual_out, y
     """Residual addition and RMS norm with MX blocks out; residual,
     residual_out, y, and codes with scales (fmt then unused) may be None."""
     R, K = int(n_rows), int(input_dim)
-    t = _mx_type(x, "x")
+    t, n = _mx_type(x, "x"), _mx_need(R, K)
     f = _mx_format(fmt) if codes is not None or scales is not None else 0
-    _mx_values(x, x.dtype, "x", R, K)
-    _mx_values(residual, x.dtype, "residual", R, K)
-    _mx_values(weight, x.dtype, "weight", 1, K)
-    _mx_values(residual_out, x.dtype, "residual_out", R, K)
-    _mx_values(y, x.dtype, "y", R, K)
-    _mx_codes(codes, scales, fmt, R, K, "")
-    _check(lib().mx_rmsnorm(_ptr(x), _ptr(residual), _ptr(weight), float(eps), t, R, K,
-                            _ptr(residual_out), _ptr(y), f, _ptr(codes), _ptr(scales),
-                            _stream(stream)), "mx_rmsnorm")
+    d = x.dtype
+    rc = lib().mx_rmsnorm(_arg(x, d, "x", n), _arg(residual, d, "residual", n),
+                          _arg(weight, d, "weight", K if n else 0), float(eps), t, R, K,
+                          _arg(residual_out, d, "residual_out", n), _arg(y, d, "y", n), f,
+                          _arg(codes, torch.uint8, "codes", n * f // 8),
+                          _arg(scales, torch.uint8, "scales", n // 32), _stream(stream))
+    _check(rc, "mx_rmsnorm")
     return codes, scales
 
 
@@ -450,12 +451,13 @@ def mxfp4_matmul(a_codes, a_scales, a_fmt, w_codes, w_scales, n_tokens, input_di
                  stream=None):
     """Y = A W^T of MX activations (a_fmt "fp8" or "fp4") and MXFP4 weights."""
     M, K, N = int(n_tokens), int(input_dim), int(output_dim)
-    t, f = _mx_type(Y, "Y"), _mx_format(a_fmt)
-    _mx_codes(a_codes, a_scales, a_fmt, M, K, "a_")
-    _mx_codes(w_codes, w_scales, "fp4", N, K, "w_")
-    _mx_values(Y, Y.dtype, "Y", M, N)
-    _check(lib().mxfp4_matmul(_ptr(a_codes), _ptr(a_scales), f, _ptr(w_codes), _ptr(w_scales),
-                              M, K, N, _ptr(Y), t, _stream(stream)), "mxfp4_matmul")
+    t, f, a, w = _mx_type(Y, "Y"), _mx_format(a_fmt), _mx_need(M, K), _mx_need(N, K)
+    rc = lib().mxfp4_matmul(_arg(a_codes, torch.uint8, "a_codes", a * f // 8),
+                            _arg(a_scales, torch.uint8, "a_scales", a // 32), f,
+                            _arg(w_codes, torch.uint8, "w_codes", w // 2),
+                            _arg(w_scales, torch.uint8, "w_scales", w // 32), M, K, N,
+                            _arg(Y, Y.dtype, "Y", M * N if a and w else 0), t, _stream(stream))
+    _check(rc, "mxfp4_matmul")
     return Y
 
 
@@ -471,19 +473,19 @@ def mxfp4_moe(x, router, router_bias, up_codes, up_scales, down_codes, down_scal
               input_dim, ffn_dim, n_experts, top_k, y, workspace, stream=None):
     """A mixture-of-experts layer with MXFP4 experts; router_bias may be None."""
     T, H, F, E, k = int(n_tokens), int(input_dim), int(ffn_dim), int(n_experts), int(top_k)
-    t = _mx_type(x, "x")
-    _mx_values(x, x.dtype, "x", T, H)
-    _mx_values(router, x.dtype, "router", E, H)
-    _expect(router_bias, torch.float32, "router_bias", max(E, 0))
-    _mx_codes(up_codes, up_scales, "fp4", E * 2 * F, H, "up_")
-    _mx_codes(down_codes, down_scales, "fp4", E * H, F, "down_")
-    _mx_values(y, x.dtype, "y", T, H)
-    _expect(workspace, torch.uint8, "workspace")
-    _check(lib().mxfp4_moe(_ptr(x), t, _ptr(router), _ptr(router_bias), _ptr(up_codes),
-                           _ptr(up_scales), _ptr(down_codes), _ptr(down_scales), T, H, F, E, k,
-                           _ptr(y), _ptr(workspace),
-                           0 if workspace is None else workspace.numel(), _stream(stream)),
-           "mxfp4_moe")
+    t, d, u8 = _mx_type(x, "x"), x.dtype, torch.uint8
+    n = _mx_need(T, H)
+    up = _mx_need(E * 2 * F, H) if F > 0 else 0
+    down = _mx_need(E * H, F) if H > 0 else 0
+    rc = lib().mxfp4_moe(_arg(x, d, "x", n), t, _arg(router, d, "router", _mx_need(E, H)),
+                         _arg(router_bias, torch.float32, "router_bias", max(E, 0)),
+                         _arg(up_codes, u8, "up_codes", up // 2),
+                         _arg(up_scales, u8, "up_scales", up // 32),
+                         _arg(down_codes, u8, "down_codes", down // 2),
+                         _arg(down_scales, u8, "down_scales", down // 32), T, H, F, E, k,
+                         _arg(y, d, "y", n), _arg(workspace, u8, "workspace", 0),
+                         0 if workspace is None else workspace.numel(), _stream(stream))
+    _check(rc, "mxfp4_moe")
     return y
 
 

@@ -204,38 +204,39 @@ __device__ __forceinline__ void set_columns(Columns<XC> &x, F source, int64_t K)
   }
 }
 
-// The products of steps first .. last-1 of one wave, through a ring of S
-// stages of its own in LDS at `ring` (no barrier), the scales of four steps
-// behind them.  ALIGNED: rows of whole steps whose scales start at dwords;
+// The products of steps first .. last-1 of one wave, through rings of its own
+// in LDS at `ring` (no barrier): SX stages of activations, which come from
+// cache, SW of weights, which come from memory, and the scales of four steps.  ALIGNED: rows of whole steps whose scales start at dwords;
 // others come through registers, whose wait also waits for what is in flight.
-template <int V, int NRV, int XC, int NP, int S, bool ALIGNED> struct MoeRing {
+template <int V, int NRV, int XC, int NP, int SW, int SX, bool ALIGNED> struct MoeRing {
   static constexpr int kTiles = V * NRV, kLoads = kTiles + XC * NP;
-  static constexpr int kBytes = (S * kLoads + V) * 1024;
-  static_assert((S == 2 || S == 3) && NRV <= 4, "");
+  static constexpr int kBytes = (SW * kTiles + SX * XC * NP + V) * 1024;
+  static_assert((SX == 2 || (SX == 3 && SW == 3)) && SW >= SX && NRV <= 4, "");
 };
 // The first stages' weights are sent for before `columns(x)` says where the
 // activations are, or that there are none (false, which is the result then).
-template <int V, int NRV, int XC, int NP, int S, bool ALIGNED, class F>
+template <int V, int NRV, int XC, int NP, int SW, int SX, bool ALIGNED, class F>
 __device__ __forceinline__ bool moe_stream(uint8_t *ring, const Rows<V, NRV> &w, Columns<XC> &x,
                                            F columns, int nb, int first, int last,
                                            f32x4 (&acc)[V * NRV]) {
-  typedef MoeRing<V, NRV, XC, NP, S, ALIGNED> R;
+  typedef MoeRing<V, NRV, XC, NP, SW, SX, ALIGNED> R;
   constexpr int kLoads = R::kLoads;
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  constexpr int kX = XC * NP * 1024, kWeights = SX * kX, kScales = kWeights + SW * R::kTiles * 1024;
   const uint32_t to_ring = lds_address(ring);
-  uint8_t *const scales = ring + S * kLoads * 1024;
+  uint8_t *const scales = ring + kScales;
 #pragma unroll
   for (int i = 0; i < R::kTiles; i++) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   const auto issue_w = [&](int s, int buf) {
-    const uint32_t to = to_ring + buf * (kLoads * 1024);
+    const uint32_t to = to_ring + kWeights + buf * (R::kTiles * 1024);
     const bool in_w = ALIGNED || 4 * s + tile_chunk<MX_FP4>(lane) < nb;
 #pragma unroll
     for (int i = 0; i < R::kTiles; i++)
       load16_to_lds(w.codes[i / NRV], in_w ? w.code_at[i] + 64u * s : kPastEnd,
-                    to + (XC * NP + i) * 1024);
+                    to + i * 1024);
   };
   const auto issue_x = [&](int s, int buf) {
-    const uint32_t to = to_ring + buf * (kLoads * 1024);
+    const uint32_t to = to_ring + buf * kX;
 #pragma unroll
     for (int i = 0; i < XC; i++) {
       const int chunk = (lane & 15) ^ ((4 * i + (lane >> 4)) & 7);
@@ -256,14 +257,14 @@ __device__ __forceinline__ bool moe_stream(uint8_t *ring, const Rows<V, NRV> &w,
 #pragma unroll
     for (int v = 0; v < V; v++)
       load16_to_lds(w.scales[v], lane < 16 * NRV ? w.scale_at[v] + 4u * s : kPastEnd,
-                    to_ring + (S * kLoads + v) * 1024);
+                    to_ring + kScales + v * 1024);
   };
   if (first < last) {
     if constexpr (ALIGNED) issue_scales(first);
     else load_scales(first);
   }
 #pragma unroll
-  for (int d = 0; d < S - 1; d++)
+  for (int d = 0; d < SW - 1; d++)
     if (first + d < last) issue_w(first + d, d);
   if (!columns(x)) {
     wait_loads<0>();
@@ -271,9 +272,9 @@ __device__ __forceinline__ bool moe_stream(uint8_t *ring, const Rows<V, NRV> &w,
   }
   if (first >= last) return true;
 #pragma unroll
-  for (int d = 0; d < S - 1; d++)
+  for (int d = 0; d < SX - 1; d++)
     if (first + d < last) issue_x(first + d, d);
-  int buf = 0;
+  int buf = 0, xbuf = 0;
   uint32_t sc[R::kTiles];
   // Not unrolled: a workgroup runs few steps, and code that is fetched for
   // one use costs more than the loop.
@@ -285,23 +286,28 @@ __device__ __forceinline__ bool moe_stream(uint8_t *ring, const Rows<V, NRV> &w,
       if constexpr (ALIGNED) issue_scales(s + 3);
       else load_scales(s + 3);
     }
-    if (s + S - 1 < last) {
-      issue_w(s + S - 1, buf == 0 ? S - 1 : buf - 1);
-      issue_x(s + S - 1, buf == 0 ? S - 1 : buf - 1);
-    }
-    // The scales of the steps from s on are older than stage s; younger are
-    // the stages ahead, of which the second one's weights (S = 3) are older
-    // than the first one's activations.
-    const int ahead = last - 1 - s;
-    constexpr int kSecond = S == 3 ? XC * NP : kLoads;
-    if (s == first) {
-      if (S == 3 && ahead >= 2) wait_loads<kSecond + kLoads>();
-      else if (ahead >= 1) wait_loads<kSecond>();
+    const bool more_w = s + SW - 1 < last, more_x = s + SX - 1 < last;
+    if (more_w) issue_w(s + SW - 1, buf == 0 ? SW - 1 : buf - 1);
+    if (more_x) issue_x(s + SX - 1, xbuf == 0 ? SX - 1 : xbuf - 1);
+    // Until step s's activations are there; its weights and scales are older.
+    // Younger are the loads of the SX - 1 steps up to this one, and of the
+    // first stages the activations alone.
+    constexpr int kFew = XC * NP;
+    if constexpr (SX == 2) {
+      if (more_w) wait_loads<kLoads>();
+      else if (more_x) wait_loads<kFew>();
       else wait_loads<0>();
     } else {
-      if (S == 3 && ahead >= 2) wait_loads<(S - 1) * kLoads>();
-      else if (ahead >= 1) wait_loads<kLoads>();
-      else wait_loads<0>();
+      const bool second = s + 1 < last;
+      if (s == first) {
+        if (more_x) wait_loads<kFew + kLoads>();
+        else if (second) wait_loads<kFew>();
+        else wait_loads<0>();
+      } else {
+        if (more_x) wait_loads<2 * kLoads>();
+        else if (second) wait_loads<kLoads>();
+        else wait_loads<0>();
+      }
     }
     if (j4 == 0) {
       if constexpr (!ALIGNED) {
@@ -316,19 +322,19 @@ __device__ __forceinline__ bool moe_stream(uint8_t *ring, const Rows<V, NRV> &w,
         sc[i] = byte_of_four(*reinterpret_cast<const u32x4 *>(scales + i / NRV * 1024 +
                                                               i % NRV * 256 + r * 16), which);
     }
-    const uint8_t *st = ring + buf * (kLoads * 1024);
+    const uint8_t *xs = ring + xbuf * kX, *ws = ring + kWeights + buf * (R::kTiles * 1024);
     const int column = XC == 4 ? r : r % (4 * XC);  // the others' results are not used
     bf16x8 b[NP][4];
 #pragma unroll
     for (int q = 0; q < NP; q++)
 #pragma unroll
       for (int j = 0; j < 4; j++)
-        b[q][j] = *reinterpret_cast<const bf16x8 *>(st + q * (XC * 1024) + column * 256 +
+        b[q][j] = *reinterpret_cast<const bf16x8 *>(xs + q * (XC * 1024) + column * 256 +
                                                     16 * ((4 * g + j) ^ (column & 7)));
 #pragma unroll
     for (int i = 0; i < R::kTiles; i++) {
       bf16x8 a[4];
-      decode_block(read_operand<MX_FP4>(st + (XC * NP + i) * 1024, operand_at<MX_FP4>(r, g)).v,
+      decode_block(read_operand<MX_FP4>(ws + i * 1024, operand_at<MX_FP4>(r, g)).v,
                    (sc[i] >> (8 * j4)) & 255u, a);
 #pragma unroll
       for (int q = 0; q < NP; q++)
@@ -336,7 +342,8 @@ __device__ __forceinline__ bool moe_stream(uint8_t *ring, const Rows<V, NRV> &w,
         for (int j = 0; j < 4; j++)
           acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[j], b[q][j], acc[i], 0, 0, 0);
     }
-    buf = buf == S - 1 ? 0 : buf + 1;
+    buf = buf == SW - 1 ? 0 : buf + 1;
+    xbuf = xbuf == SX - 1 ? 0 : xbuf + 1;
   }
   wait_lds();
   return true;
@@ -403,7 +410,7 @@ __device__ __forceinline__ int count_before(const uint32_t *row, int from, int t
 // are the chosen ones and give each slot exactly one writer.
 template <int NPX, int NPH, int NF, int XC, int W, int S, bool ALIGNED>
 __global__ __launch_bounds__(W * 64) void moe_up_kernel(UpArgs p) {
-  typedef MoeRing<2, NF, XC, NPX, S, ALIGNED> Ring;
+  typedef MoeRing<2, NF, XC, NPX, S, S, ALIGNED> Ring;
   constexpr int kThreads = W * 64;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[W * Ring::kBytes];
   extern __shared__ u32x4 key_lds[];  // the logits' keys [T][key_stride(E)]
@@ -492,7 +499,7 @@ __global__ __launch_bounds__(W * 64) void moe_up_kernel(UpArgs p) {
       set_columns(c, [&](int i) { return base + i < n ? list[base + i] & 255 : -1; }, p.H);
       return true;
     };
-    if (!moe_stream<2, NF, XC, NPX, S, ALIGNED>(mine, w, x, columns, nb, first, last, acc)) break;
+    if (!moe_stream<2, NF, XC, NPX, S, S, ALIGNED>(mine, w, x, columns, nb, first, last, acc)) break;
     keep_sums(mine, acc);
     __syncthreads();
     for (int i = wave; i < NF; i += W) {
@@ -543,10 +550,10 @@ struct DownArgs {
 // unweighted, by slot.  The workgroup that finds itself the last of its rows
 // then adds up the slots of every token, in the order of their ranks and with
 // the softmax's weights.
-template <int TY, int NR, int XC, int W, int S, bool ALIGNED>
+template <int TY, int NR, int XC, int W, int SW, int SX, bool ALIGNED>
 __global__ __launch_bounds__(W * 64) void moe_down_kernel(DownArgs p) {
   constexpr int NPH = kHParts<TY>;
-  typedef MoeRing<1, NR, XC, NPH, S, ALIGNED> Ring;
+  typedef MoeRing<1, NR, XC, NPH, SW, SX, ALIGNED> Ring;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[W * Ring::kBytes];
   __shared__ int slots[kMoeTokens], last_one;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -580,7 +587,7 @@ __global__ __launch_bounds__(W * 64) void moe_down_kernel(DownArgs p) {
       set_columns(c, [&](int i) { return base + i < n ? slots[base + i] : -1; }, p.F);
       return true;
     };
-    moe_stream<1, NR, XC, NPH, S, ALIGNED>(mine, w, x, columns, nb, first, last, acc);
+    moe_stream<1, NR, XC, NPH, SW, SX, ALIGNED>(mine, w, x, columns, nb, first, last, acc);
     keep_sums(mine, acc);
     __syncthreads();
     for (int i = wave; i < NR; i += W) {
@@ -665,9 +672,9 @@ void launch(const MoeArgs &a, const Workspace &w, hipStream_t stream) {
                          dim3(tiles(a.F, NF), groups), dim3(64 * W),
                          (size_t)a.T * key_stride(a.E) * 4, stream, u);
     };
-    const auto down = [&](auto nr, auto ns) {
-      constexpr int NR = decltype(nr)::value, S = decltype(ns)::value;
-      hipLaunchKernelGGL((moe_down_kernel<TY, NR, XC, 2, S, DOWN_ALIGNED>),
+    const auto down = [&](auto nr, auto nw, auto nx) {
+      constexpr int NR = decltype(nr)::value, SW = decltype(nw)::value, SX = decltype(nx)::value;
+      hipLaunchKernelGGL((moe_down_kernel<TY, NR, XC, 2, SW, SX, DOWN_ALIGNED>),
                          dim3(tiles(a.H, NR), groups), dim3(128), 0, stream, d);
     };
     typedef std::integral_constant<int, 1> I1;
@@ -675,7 +682,8 @@ void launch(const MoeArgs &a, const Workspace &w, hipStream_t stream) {
     typedef std::integral_constant<int, 4> I4;
     // stages: three, or two where three do not fit
     typedef std::integral_constant<int, (XC * NPX < 6 ? 3 : 2)> SX;
-    typedef std::integral_constant<int, (XC * NPH < 6 || NPH == 2 ? 3 : 2)> SH;
+    typedef std::integral_constant<int, (XC == 4 ? (NPH == 2 ? 5 : 3) : 3)> SHW;
+    typedef std::integral_constant<int, (XC == 4 || XC * NPH == 6 ? 2 : 3)> SHX;
     constexpr int kWide = NPX * XC < 12 ? 4 : 2;
     if ((int64_t)tiles(a.F, kWide) * groups >= 512)
       up(std::integral_constant<int, kWide>{}, I2{}, SX{});
@@ -683,8 +691,8 @@ void launch(const MoeArgs &a, const Workspace &w, hipStream_t stream) {
       up(I2{}, I2{}, SX{});
     else
       up(I1{}, std::integral_constant<int, (XC == 1 ? 4 : 2)>{}, SX{});
-    if ((int64_t)tiles(a.H, 4) * groups >= 512) down(I4{}, SH{});
-    else down(I2{}, SH{});
+    if ((int64_t)tiles(a.H, 4) * groups >= 512) down(I4{}, SHW{}, SHX{});
+    else down(I2{}, SHW{}, SHX{});
   };
   // Columns at a time: all of up to four tokens; eight for up to two tokens an
   // expert (an expert that more than eight chose takes its weights again for
