@@ -11,6 +11,7 @@ namespace q4k {
 // compiler does not count these loads (they have no destination register);
 // wait_loads does.  Nothing else in the kernels that include this uses m0.
 __device__ __forceinline__ void load16_to_lds(i32x4 view, uint32_t offset, uint32_t lds) {
+  lds = __builtin_amdgcn_readfirstlane(lds);  // a scalar already, wherever it is kept
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                :
                : "s"(lds), "v"(offset), "s"(view)

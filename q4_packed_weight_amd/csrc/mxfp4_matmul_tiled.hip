@@ -22,13 +22,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mxfp4_tiled_kernel(
   constexpr int BM = 16 * WM * TM, BN = 16 * WN * TN;
   constexpr int AP = kTileLoads<AF>;
   constexpr int kStepLoads = BM / 16 * AP + BN / 16;      // 1 KiB each
-  constexpr int kMine = kStepLoads / kW;
+  constexpr int kMine = kStepLoads / kW;                  // of a wave, tokens first
+  constexpr int kMineA = BM / 16 * AP / kW;
   constexpr int kStep = kStepLoads * 1024;
   // Scales are kept for kChunk steps at a time, 4 kChunk bytes a row.
   constexpr int kChunk = KS == 2 ? 8 : 4;
   constexpr int kScales = (BM + BN) * 4 * kChunk;
   constexpr int kScaleLoads = kScales / 1024 / kW;        // of a wave
-  static_assert(kStepLoads % kW == 0 && BM % 64 == 0 && BN % 64 == 0, "whole loads");
+  static_assert(BM / 16 * AP % kW == 0 && BN / 16 % kW == 0 && BM % 64 == 0 && BN % 64 == 0,
+                "whole loads");
   static_assert(!kHalves || (KS == 1 && S == 3 && BM + BN <= kThreads), "");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S * KS * kStep + 2 * kScales];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -63,7 +65,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mxfp4_tiled_kernel(
 #pragma unroll
   for (int i = 0; i < kMine; i++) {
     const int p = i * kW + wave;
-    if (p < BM / 16 * AP)
+    if (i < kMineA)
       offset[i] = (uint32_t)token(p * (16 / AP) + tile_row<AF>(lane)) * a_bytes +
                   16 * tile_chunk<AF>(lane);
     else
@@ -79,7 +81,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mxfp4_tiled_kernel(
 #pragma unroll
       for (int i = 0; i < kMine; i++) {
         const int p = i * kW + wave;
-        const bool is_a = p < BM / 16 * AP;
+        const bool is_a = i < kMineA;
         uint32_t o = offset[i] + (uint32_t)s * (is_a ? 64 * AP : 64);
         if (KS > 1 || 4 * s + 4 > nb) {
           const int block = is_a ? chunk_block<AF>(tile_chunk<AF>(lane)) : tile_chunk<MX_FP4>(lane);
@@ -281,6 +283,43 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mxfp4_tiled_kernel(
   }
 
   const bool wide = N % 8 == 0 && (reinterpret_cast<uintptr_t>(y) & 15) == 0;
+  const auto pair = [&](int i, int j, float (&f)[8]) {
+#pragma unroll
+    for (int q = 0; q < 4; q++) {
+      f[q] = acc[i][j][q];
+      f[4 + q] = acc[i][j + 1][q];
+    }
+  };
+  if (TN >= 4 && wide && rows_m == BM && rows_n == BN) {
+    // Whole tiles go out through LDS, 16 tokens at a time in a part of the
+    // wave's own, so that a store covers whole cache lines of a token's row:
+    // straight from registers it covers 64 bytes of 16 rows (4096x128x16384,
+    // 134 MB of bf16 outputs: 64 us).
+    constexpr int kSize = T == MX_F32 ? 4 : 2, kRow = 16 * TN * kSize, kStride = kRow + 16;
+    constexpr int kLanes = kRow / 16, kTokens = 64 / kLanes;  // of a store
+    static_assert(kW * 16 * kStride <= (int)sizeof(lds) || TN < 4, "");
+    lds_barrier();  // every wave's operands are read
+#pragma unroll
+    for (int i = 0; i < TM; i++) {
+      uint8_t *const part = lds + wave * (16 * kStride);
+#pragma unroll
+      for (int j = 0; j < TN; j += 2) {
+        float f[8];
+        pair(i, j, f);
+        store_raw8<T>(part + r * kStride + (16 * j + 8 * g) * kSize, 0, f32_to_raw8<T>(f));
+      }
+      wait_lds();
+#pragma unroll
+      for (int q = 0; q < 16 / kTokens; q++) {
+        const int t = q * kTokens + lane / kLanes, at = lane % kLanes * 16;
+        const u32x4 v = *reinterpret_cast<const u32x4 *>(part + t * kStride + at);
+        uint8_t *const row = static_cast<uint8_t *>(y) +
+                             ((int64_t)(m0 + (wm * TM + i) * 16 + t) * N + n0 + wn * 16 * TN) * kSize;
+        *reinterpret_cast<u32x4 *>(row + at) = v;
+      }
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < TM; i++) {
     const int m = (wm * TM + i) * 16 + r;
@@ -289,11 +328,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mxfp4_tiled_kernel(
     for (int j = 0; j < TN; j += 2) {
       const int n = (wn * TN + j) * 16 + 8 * g;
       float f[8];
-#pragma unroll
-      for (int q = 0; q < 4; q++) {
-        f[q] = acc[i][j][q];
-        f[4 + q] = acc[i][j + 1][q];
-      }
+      pair(i, j, f);
       store_row8<T>(y, (int64_t)(m0 + m) * N + n0 + n, f, rows_n - n, wide);
     }
   }
