@@ -267,3 +267,23 @@ def test_moe_workspace_is_left_to_itself(T):
     layer.x = x
     for _ in range(10):
         assert torch.equal(layer.run(), first)
+
+
+# ------------------------------------------------------------ all of them together
+
+def test_example_layer():
+    """examples/mx_layer.py: norm, product, norm and experts, captured and
+    replayed.  bf16 outputs are off by at most 2^-9 of each value, and by less
+    in the norm; a choice of experts that fp32 logits take differently than 64
+    bits is not among these few tokens."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "mx_layer.py")
+    spec = importlib.util.spec_from_file_location("mx_layer", path)
+    mx_layer = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mx_layer)
+    torch.manual_seed(5)
+    for error, product in mx_layer.main(["--tokens", "1", "5", "24", "--dim", "512", "--ffn", "256",
+                                         "--experts", "12", "--top-k", "3"]):
+        assert error <= 2.0 ** -8 and product <= 2.0 ** -8
