@@ -83,14 +83,17 @@ template <int T> __device__ __forceinline__ Raw8<T> f32_to_raw8(const float (&f)
   return r;
 }
 
-template <int T> __device__ __forceinline__ void store_raw8(void *p, int64_t chunk,
-                                                            const Raw8<T> &r) {
-  u32x4 *q = reinterpret_cast<u32x4 *>(p);
-  if constexpr (T == MX_F32) {
-    q[2 * chunk] = r.v;
-    q[2 * chunk + 1] = r.w;
+// ONCE: past the caches (the non-temporal hint), for outputs that are larger
+// than what the L2s keep until their next use.
+template <int T, bool ONCE = false>
+__device__ __forceinline__ void store_raw8(void *p, int64_t chunk, const Raw8<T> &r) {
+  u32x4 *q = reinterpret_cast<u32x4 *>(p) + (T == MX_F32 ? 2 * chunk : chunk);
+  if constexpr (ONCE) {
+    __builtin_nontemporal_store(r.v, q);
+    if constexpr (T == MX_F32) __builtin_nontemporal_store(r.w, q + 1);
   } else {
-    q[chunk] = r.v;
+    *q = r.v;
+    if constexpr (T == MX_F32) q[1] = r.w;
   }
 }
 

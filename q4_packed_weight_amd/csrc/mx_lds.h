@@ -7,15 +7,22 @@
 namespace q4k {
 
 // One piece per lane from a buffer view straight into LDS: lane l's lands at
-// lds + 16 l (lds + 4 l), zeros where the offset is past the view's end.  The
-// compiler does not count these loads (they have no destination register);
-// wait_loads does.  Nothing else in the kernels that include this uses m0.
+// lds + 16 l, zeros where the offset is past the view's end.  ONCE: with the
+// non-temporal hint.  The compiler does not count these loads (they have no
+// destination register); wait_loads does.  Nothing else in the kernels that
+// include this uses m0.
+template <bool ONCE = false>
 __device__ __forceinline__ void load16_to_lds(i32x4 view, uint32_t offset, uint32_t lds) {
-  lds = __builtin_amdgcn_readfirstlane(lds);  // a scalar already, wherever it is kept
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               :
-               : "s"(lds), "v"(offset), "s"(view)
-               : "memory");
+  if constexpr (ONCE)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds"
+                 :
+                 : "s"(lds), "v"(offset), "s"(view)
+                 : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(lds), "v"(offset), "s"(view)
+                 : "memory");
 }
 
 // Until no more than N of the wave's loads are outstanding.

@@ -26,7 +26,7 @@ __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const void *x, in
   }
 }
 
-template <int T, int FMT>
+template <int T, int FMT, bool ONCE>
 __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(const uint8_t *codes,
                                                                  const uint8_t *scales,
                                                                  int64_t n_chunks, void *y) {
@@ -37,7 +37,7 @@ __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(const uint8_t *
     else q = reinterpret_cast<const u32x2 *>(codes)[c];
     float f[8];
     mx_decode8<FMT>(q, mx_scale_value(scales[c >> 2]), f);
-    store_raw8<T>(y, c, f32_to_raw8<T>(f));
+    store_raw8<T, ONCE>(y, c, f32_to_raw8<T>(f));
   }
 }
 
@@ -72,9 +72,14 @@ hipError_t mx_dequantize_launch(const uint8_t *codes, const uint8_t *scales, int
                                 int64_t n_rows, int64_t K, void *y, int type,
                                 hipStream_t stream) {
   const int64_t n = n_rows * (K / 8);
-#define CALL(T, F)                                                                         \
-  hipLaunchKernelGGL((mx_dequantize_kernel<T, F>), dim3(grid_for(n)), dim3(kThreads), 0,   \
-                     stream, codes, scales, n, y)
+  const bool once = n * (type == MX_F32 ? 32 : 16) >= kMxOnceBytes;
+#define CALL(T, F)                                                                             \
+  if (once)                                                                                    \
+    hipLaunchKernelGGL((mx_dequantize_kernel<T, F, true>), dim3(grid_for(n)), dim3(kThreads),  \
+                       0, stream, codes, scales, n, y);                                        \
+  else                                                                                         \
+    hipLaunchKernelGGL((mx_dequantize_kernel<T, F, false>), dim3(grid_for(n)), dim3(kThreads), \
+                       0, stream, codes, scales, n, y)
   Q4K_BY_TYPE(type, format, CALL)
 #undef CALL
   return hipGetLastError();

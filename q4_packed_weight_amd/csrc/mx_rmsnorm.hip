@@ -1,4 +1,6 @@
 // mx_rmsnorm.hip -- residual addition, root-mean-square norm, MX blocks out.
+#include <type_traits>
+
 #include "mx_common.h"
 #include "mx_internal.h"
 
@@ -39,7 +41,7 @@ __device__ __forceinline__ float sum_squares(const Raw8<T> &r) {
 }
 
 // Eight normed values: y and the codes of their block.
-template <int T>
+template <int T, bool ONCE>
 __device__ __forceinline__ void emit8(const Raw8<T> &r, const Raw8<T> &w, float inv, int64_t chunk,
                                       void *y, int format, uint8_t *codes, uint8_t *scales) {
   float f[8], g[8];
@@ -47,7 +49,7 @@ __device__ __forceinline__ void emit8(const Raw8<T> &r, const Raw8<T> &w, float 
   raw8_to_f32<T>(w, g);
 #pragma unroll
   for (int i = 0; i < 8; i++) f[i] = f[i] * inv * g[i];
-  if (y) store_raw8<T>(y, chunk, f32_to_raw8<T>(f));
+  if (y) store_raw8<T, ONCE>(y, chunk, f32_to_raw8<T>(f));
   if (format == MX_FP8) {
     const uint32_t s = mx_scale_byte<MX_FP8>(block_amax_bits(f));
     reinterpret_cast<u32x2 *>(codes)[chunk] = mx_encode8<MX_FP8>(f, s);
@@ -61,12 +63,12 @@ __device__ __forceinline__ void emit8(const Raw8<T> &r, const Raw8<T> &w, float 
 
 // One row per workgroup, held in registers as NC chunks of eight values per
 // lane, so memory is read once; four neighbouring lanes hold one block.
-template <int T, int NC>
+template <int T, int NC, bool ONCE>
 __global__ __launch_bounds__(1024) void mx_rmsnorm_kernel(const void *x, const void *residual,
                                                           const void *weight, float eps, int n,
                                                           float inv_dim, void *residual_out,
-                                                          void *y, int format, uint8_t *codes,
-                                                          uint8_t *scales) {
+                                                          void *y, int format,
+                                                          uint8_t *codes, uint8_t *scales) {
   __shared__ float lds[16];
   const int64_t base = (int64_t)blockIdx.x * n;  // chunk index of the row's first
   Raw8<T> r[NC], w[NC];
@@ -93,8 +95,8 @@ __global__ __launch_bounds__(1024) void mx_rmsnorm_kernel(const void *x, const v
   for (int j = 0; j < NC; j++) {
     const int c = threadIdx.x + j * blockDim.x;
     if (c < n) {
-      if (residual_out) store_raw8<T>(residual_out, base + c, r[j]);
-      emit8<T>(r[j], w[j], inv, base + c, y, format, codes, scales);
+      if (residual_out) store_raw8<T, ONCE>(residual_out, base + c, r[j]);
+      emit8<T, ONCE>(r[j], w[j], inv, base + c, y, format, codes, scales);
     }
   }
 }
@@ -102,7 +104,7 @@ __global__ __launch_bounds__(1024) void mx_rmsnorm_kernel(const void *x, const v
 // Rows too long for registers: one pass for the sum, one for the outputs.
 // Each lane writes only the chunks of residual_out that it reads again
 // itself, so residual_out may be x or residual.
-template <int T>
+template <int T, bool ONCE>
 __global__ __launch_bounds__(1024) void mx_rmsnorm_long_kernel(
     const void *x, const void *residual, const void *weight, float eps, int n, float inv_dim,
     void *residual_out, void *y, int format, uint8_t *codes, uint8_t *scales) {
@@ -118,8 +120,8 @@ __global__ __launch_bounds__(1024) void mx_rmsnorm_long_kernel(
   for (int c = threadIdx.x; c < n; c += blockDim.x) {
     Raw8<T> r = load_raw8<T>(x, base + c);
     if (residual) r = add_raw8<T>(r, load_raw8<T>(residual, base + c));
-    if (residual_out) store_raw8<T>(residual_out, base + c, r);
-    emit8<T>(r, load_raw8<T>(weight, c), inv, base + c, y, format, codes, scales);
+    if (residual_out) store_raw8<T, ONCE>(residual_out, base + c, r);
+    emit8<T, ONCE>(r, load_raw8<T>(weight, c), inv, base + c, y, format, codes, scales);
   }
 }
 
@@ -130,29 +132,34 @@ hipError_t mx_rmsnorm_launch(const void *x, const void *residual, const void *we
                              int format, uint8_t *codes, uint8_t *scales, hipStream_t stream) {
   const int n = (int)(K / 8);
   const float inv_dim = 1.0f / (float)K;
+  const bool once = n_rows * K * (type == MX_F32 ? 4 : 2) >= kMxOnceBytes;
   // chunks per lane: one up to 1024 chunks, two, then four
   const int nc = n <= 1024 ? 1 : n <= 2048 ? 2 : 4;
   const int lanes = (n + nc - 1) / nc;
   const int threads = lanes >= 1024 ? 1024 : (lanes + 63) / 64 * 64;
   // Rows beyond 2^31 - 1 of a grid never occur: their codes alone would not
   // fit the GPU.
-#define ARGS x, residual, weight, eps, n, inv_dim, residual_out, y, format, codes, scales
-#define CALL(T)                                                                                   \
-  if (n > 4096)                                                                                   \
-    hipLaunchKernelGGL((mx_rmsnorm_long_kernel<T>), dim3(n_rows), dim3(1024), 0, stream, ARGS);   \
-  else if (nc == 1)                                                                               \
-    hipLaunchKernelGGL((mx_rmsnorm_kernel<T, 1>), dim3(n_rows), dim3(threads), 0, stream, ARGS);  \
-  else if (nc == 2)                                                                               \
-    hipLaunchKernelGGL((mx_rmsnorm_kernel<T, 2>), dim3(n_rows), dim3(threads), 0, stream, ARGS);  \
-  else                                                                                            \
-    hipLaunchKernelGGL((mx_rmsnorm_kernel<T, 4>), dim3(n_rows), dim3(threads), 0, stream, ARGS)
+  const auto run = [&](auto t, auto o) {
+    constexpr int T = decltype(t)::value;
+    constexpr bool ONCE = decltype(o)::value;
+    const auto go = [&](auto kernel, int block) {
+      hipLaunchKernelGGL(kernel, dim3(n_rows), dim3(block), 0, stream, x, residual, weight, eps, n,
+                         inv_dim, residual_out, y, format, codes, scales);
+    };
+    if (n > 4096) go(mx_rmsnorm_long_kernel<T, ONCE>, 1024);
+    else if (nc == 1) go(mx_rmsnorm_kernel<T, 1, ONCE>, threads);
+    else if (nc == 2) go(mx_rmsnorm_kernel<T, 2, ONCE>, threads);
+    else go(mx_rmsnorm_kernel<T, 4, ONCE>, threads);
+  };
+  const auto by_size = [&](auto t) {
+    if (once) run(t, std::true_type{});
+    else run(t, std::false_type{});
+  };
   switch (type) {
-    case MX_F32: CALL(MX_F32); break;
-    case MX_BF16: CALL(MX_BF16); break;
-    default: CALL(MX_F16); break;
+    case MX_F32: by_size(std::integral_constant<int, MX_F32>{}); break;
+    case MX_BF16: by_size(std::integral_constant<int, MX_BF16>{}); break;
+    default: by_size(std::integral_constant<int, MX_F16>{}); break;
   }
-#undef CALL
-#undef ARGS
   return hipGetLastError();
 }
 

@@ -294,7 +294,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mxfp4_tiled_kernel(
     // Whole tiles go out through LDS, 16 tokens at a time in a part of the
     // wave's own, so that a store covers whole cache lines of a token's row:
     // straight from registers it covers 64 bytes of 16 rows (4096x128x16384,
-    // 134 MB of bf16 outputs: 64 us).
+    // 134 MB of bf16 outputs: 64 us, so 48).  Past the caches, 43 us: the
+    // kernel's end does not wait for their lines to be written back.
     constexpr int kSize = T == MX_F32 ? 4 : 2, kRow = 16 * TN * kSize, kStride = kRow + 16;
     constexpr int kLanes = kRow / 16, kTokens = 64 / kLanes;  // of a store
     static_assert(kW * 16 * kStride <= (int)sizeof(lds) || TN < 4, "");
@@ -315,7 +316,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mxfp4_tiled_kernel(
         const u32x4 v = *reinterpret_cast<const u32x4 *>(part + t * kStride + at);
         uint8_t *const row = static_cast<uint8_t *>(y) +
                              ((int64_t)(m0 + (wm * TM + i) * 16 + t) * N + n0 + wn * 16 * TN) * kSize;
-        *reinterpret_cast<u32x4 *>(row + at) = v;
+        __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(row + at));
       }
     }
     return;

@@ -214,7 +214,8 @@ __device__ __forceinline__ void set_columns(Columns<XC> &x, F source, int64_t K)
 // it, which long rows feel (the loads alone of 499 MB of gate and up rows of
 // 4096: 121 against 105 us); but a ring of two pairs leaves less room for wide
 // tiles (32 tokens on 4 of 32 experts of 2880x2880 fp16, up: 103 us with
-// P = 1, 124 with P = 2).
+// P = 1, 124 with P = 2).  Whole lines are not kept in cache, half lines are
+// until their other half is taken.
 template <int V, int NRV, int XC, int NP, int P, int SW, int SX> struct MoeRing {
   static constexpr int kTiles = V * NRV, kX = XC * NP * 1024, kUnit = kTiles * P * 1024;
   static constexpr int kColumns = SX * kX;                                 // a wave's activations
@@ -245,9 +246,10 @@ __device__ __forceinline__ bool moe_stream(uint8_t *xring, uint8_t *ring, const 
 #pragma unroll
       for (int h = 0; h < P; h++) {
         const int row = 16 * (i % NRV) + 8 * h;
-        load16_to_lds(w.codes[i / NRV],
-                      in && row < w.rows ? w_at + (uint32_t)row * w.row_bytes + 64u * s : kPastEnd,
-                      to + (P * i + h) * 1024);
+        load16_to_lds<P == 2>(
+            w.codes[i / NRV],
+            in && row < w.rows ? w_at + (uint32_t)row * w.row_bytes + 64u * s : kPastEnd,
+            to + (P * i + h) * 1024);
       }
   };
   const auto issue_x = [&](int s, int buf) {
@@ -729,11 +731,12 @@ hipError_t launch(const MoeArgs &a, const Workspace &w, hipStream_t stream) {
     typedef std::integral_constant<int, 4> I4;
     typedef std::integral_constant<int, (kUpX < 6 ? 3 : 2)> SU;
     typedef std::integral_constant<int, (kUpX == 12 ? 2 : 4)> Wide;
-    // Pairs of steps for long rows, where a ring of them leaves wide tiles
-    // (32 tokens on 8 experts of 4096x14336 bf16: 198 us against 203).
+    // Pairs of steps for long rows and many workgroups, where a ring of them
+    // leaves wide tiles (32 tokens on 8 experts of 4096x14336 bf16: 192 us
+    // against 203; one token on 2 of them 67 against 61).
     bool done = false;
-    if constexpr (XC > 1 && kUpX <= 4) {
-      done = a.H >= 4096 && (int64_t)tiles(a.F, 3) * groups >= 512;
+    if constexpr (kUpX <= 4) {
+      done = a.H >= 4096 && (int64_t)tiles(a.F, 3) * groups >= 1024;
       if (done) up(std::integral_constant<int, 3>{}, I2{}, I2{}, I2{}, I2{});
     }
     if (done) {
@@ -749,7 +752,7 @@ hipError_t launch(const MoeArgs &a, const Workspace &w, hipStream_t stream) {
     typedef std::integral_constant<int, (kDownX == 8 ? 5 : 3)> SDW;
     typedef std::integral_constant<int, (kDownX >= 6 ? 2 : 3)> SDX;
     done = false;
-    if constexpr (XC > 1 && kDownX <= 8) {
+    if constexpr (kDownX <= 8) {
       done = a.F >= 4096 && (int64_t)tiles(a.H, 4) * groups >= 256;
       if (done) down(I4{}, I2{}, I2{}, I2{}, I2{});
     }

@@ -236,7 +236,8 @@ def test_moe_columns(T, H, F, E, k, kind):
 @pytest.mark.parametrize("T,H,F,E,k", [(32, 4096, 96, 256, 16), (9, 512, 4096, 32, 8),
                                        (24, 4128, 4160, 16, 2), (33, 1024, 2080, 16, 4),
                                        (3, 2048, 1024, 64, 8), (1, 4096, 4096, 8, 2),
-                                       (40, 4224, 1600, 16, 2)])
+                                       (40, 4224, 1600, 16, 2), (30, 4096, 160, 256, 16),
+                                       (4, 4096, 1600, 32, 8), (24, 4160, 1568, 32, 3)])
 def test_moe_tiles(T, H, F, E, k, kind):
     Layer(T, H, F, E, k, kind).check()
 
