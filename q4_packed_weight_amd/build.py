@@ -32,10 +32,6 @@ FLAGS = [
     "-Wall", "-Wno-unused-function",
     "-I", INCLUDE, "-I", CSRC,
 ]
-# The MX kernels keep their sums in ordinary registers: an empty asm statement
-# holds each product's operands until the sum is written (mx_common.h), and
-# with the sums in accumulation registers it costs a copy of them each time.
-MX_FLAGS = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
 
 
 def sources():
@@ -44,8 +40,7 @@ def sources():
 
 def _compile(src, verbose):
     obj = os.path.join(BUILD, os.path.basename(src)[:-4] + ".o")
-    extra = MX_FLAGS if os.path.basename(src).startswith("mx") else []
-    cmd = [HIPCC, *FLAGS, *extra, "-c", src, "-o", obj]
+    cmd = [HIPCC, *FLAGS, "-c", src, "-o", obj]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
