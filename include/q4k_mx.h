@@ -51,7 +51,7 @@ extern "C" {
  * zeros has scale byte 0 and codes 0 (-0 keeps its sign); a block that holds
  * a NaN or an infinity has scale byte 255 and codes 0.
  *   x          [n_rows][input_dim] of x_type, 16-byte aligned
- *   n_rows     > 0; input_dim > 0, a multiple of 32, at most 2^24
+ *   n_rows     > 0, below 2^31; input_dim > 0, a multiple of 32, at most 2^24
  *   codes      16-byte aligned, every byte written; scales likewise
  *              (any alignment)
  * Exact: the result is a function of the values alone.
@@ -99,8 +99,8 @@ int mx_rmsnorm(const void *x, const void *residual, const void *weight, float ep
  *   a_codes, a_scales  n_tokens rows of input_dim values in a_format
  *   w_codes, w_scales  output_dim rows of input_dim values in MX_FP4
  *   codes 16-byte aligned, scales any alignment
- *   n_tokens   > 0, at most 2^21; output_dim > 0; input_dim > 0, a multiple of
- *              32, at most 2^24
+ *   n_tokens   > 0, at most 2^21; output_dim > 0, at most 2^26; input_dim > 0,
+ *              a multiple of 32, at most 2^24
  *   Y          [n_tokens][output_dim] of y_type, aligned to its type
  * A NaN block makes the outputs that use it NaN.
  */
@@ -122,15 +122,17 @@ int mxfp4_matmul(const uint8_t *a_codes, const uint8_t *a_scales, int a_format,
  *              expert's rows 0 .. ffn_dim-1 gate, the others up
  *   down_codes, down_scales  MXFP4 [n_experts][input_dim][ffn_dim]
  *   input_dim, ffn_dim  > 0, multiples of 32, at most 2^20
- *   n_experts  1 .. 256; top_k 1 .. min(n_experts, 16); n_tokens > 0
+ *   n_experts  1 .. 256; top_k 1 .. min(n_experts, 16); n_tokens > 0, at most
+ *              2^21
  *   workspace  mxfp4_moe_workspace_size bytes, 256-byte aligned, of any
  *              content; its content after the call is undefined.  Calls that
  *              share one must not overlap in time.
  * e2m1 weights times their block's scale are exact in bf16; activations enter
  * as one (bf16), two (fp16) or three (fp32) bf16 values and h as two, or three
  * for fp32, so only fp32-level rounding lies between x and y (x below 2^127).
- * At most 64 tokens (fewer from 129 experts on: 8192 / n_experts) run at a
- * time, more loop over them.
+ * At most 64 tokens run at a time, more loop over them; fewer from 129 experts
+ * on (8192 / n_experts), and where top_k * max(input_dim, ffn_dim) passes 5.5
+ * million (2^31 / 6 of it, so that a group's slots stay within 31-bit offsets).
  * workspace_bytes too small gives Q4K_ESCRATCH.
  */
 int64_t mxfp4_moe_workspace_size(int64_t n_tokens, int64_t input_dim, int64_t ffn_dim,

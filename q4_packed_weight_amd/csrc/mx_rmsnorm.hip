@@ -1,4 +1,5 @@
 // mx_rmsnorm.hip -- residual addition, root-mean-square norm, MX blocks out.
+#include <algorithm>
 #include <type_traits>
 
 #include "mx_common.h"
@@ -137,14 +138,23 @@ hipError_t mx_rmsnorm_launch(const void *x, const void *residual, const void *we
   const int nc = n <= 1024 ? 1 : n <= 2048 ? 2 : 4;
   const int lanes = (n + nc - 1) / nc;
   const int threads = lanes >= 1024 ? 1024 : (lanes + 63) / 64 * 64;
-  // Rows beyond 2^31 - 1 of a grid never occur: their codes alone would not
-  // fit the GPU.
   const auto run = [&](auto t, auto o) {
     constexpr int T = decltype(t)::value;
     constexpr bool ONCE = decltype(o)::value;
+    // A grid holds fewer than 2^32 threads, and so 2^22 rows of any block.
+    constexpr int64_t kRows = ((int64_t)1 << 22) - 1;
     const auto go = [&](auto kernel, int block) {
-      hipLaunchKernelGGL(kernel, dim3(n_rows), dim3(block), 0, stream, x, residual, weight, eps, n,
-                         inv_dim, residual_out, y, format, codes, scales);
+      for (int64_t r = 0; r < n_rows; r += kRows) {
+        const int64_t at = r * K, size = T == MX_F32 ? 4 : 2;
+        const auto in = [&](const void *p) {
+          return p ? static_cast<const uint8_t *>(p) + at * size : nullptr;
+        };
+        const auto out = [&](void *p) { return p ? static_cast<uint8_t *>(p) + at * size : nullptr; };
+        hipLaunchKernelGGL(kernel, dim3(std::min(n_rows - r, kRows)), dim3(block), 0, stream, in(x),
+                           in(residual), weight, eps, n, inv_dim, out(residual_out), out(y), format,
+                           codes ? codes + at * format / 8 : nullptr,
+                           scales ? scales + at / 32 : nullptr);
+      }
     };
     if (n > 4096) go(mx_rmsnorm_long_kernel<T, ONCE>, 1024);
     else if (nc == 1) go(mx_rmsnorm_kernel<T, 1, ONCE>, threads);

@@ -171,8 +171,11 @@ bool valid_mx_type(int t) { return t == MX_F32 || t == MX_BF16 || t == MX_F16; }
 bool valid_mx_format(int f) { return f == MX_FP4 || f == MX_FP8; }
 
 // Largest n_tokens of mxfp4_matmul (64 tokens a workgroup, 65535 of them in
-// a grid's second dimension) and input_dim / ffn_dim of mxfp4_moe.
+// a grid's second dimension), output_dim of the same (16 rows to a workgroup
+// of 512 threads, of which a grid holds fewer than 2^32) and input_dim /
+// ffn_dim of mxfp4_moe.
 constexpr int64_t kMaxMxTokens = (int64_t)1 << 21;
+constexpr int64_t kMaxMxOutputDim = (int64_t)1 << 26;
 constexpr int64_t kMaxMoeDim = (int64_t)1 << 20;
 
 bool valid_moe_dims(int64_t T, int64_t H, int64_t F, int64_t E, int64_t k) {
@@ -601,7 +604,8 @@ int mx_rmsnorm(const void *x, const void *residual, const void *weight, float ep
 int mxfp4_matmul(const uint8_t *a_codes, const uint8_t *a_scales, int a_format,
                  const uint8_t *w_codes, const uint8_t *w_scales, int64_t n_tokens,
                  int64_t input_dim, int64_t output_dim, void *Y, int y_type, void *stream) {
-  if (!valid_mx_dims(output_dim, input_dim) || n_tokens <= 0 || n_tokens > kMaxMxTokens)
+  if (!valid_mx_dims(output_dim, input_dim) || output_dim > kMaxMxOutputDim || n_tokens <= 0 ||
+      n_tokens > kMaxMxTokens)
     return Q4K_EINVAL_DIM;
   if (!valid_mx_format(a_format) || !valid_mx_type(y_type)) return Q4K_EINVAL_TYPE;
   if (!a_codes || !a_scales || !w_codes || !w_scales || !Y) return Q4K_ENULL;

@@ -106,6 +106,10 @@ def test_rejects_bad_row_counts(lib, n):
     assert lib.mxfp4_moe(A, F32, B, None, C, D, C, D, n, 64, 64, 4, 2, E, A, 1 << 40, None) == -1
 
 
+def test_matmul_rejects_more_outputs_than_a_grid(lib):
+    assert lib.mxfp4_matmul(A, B, FP8, C, D, 4, 64, (1 << 26) + 1, E, F32, None) == -1
+
+
 @pytest.mark.parametrize("experts,top_k", [(0, 1), (257, 2), (4, 0), (4, 5), (64, 17), (-3, -4)])
 def test_moe_rejects_bad_routing(lib, experts, top_k):
     assert lib.mxfp4_moe(A, F32, B, None, C, D, C, D, 4, 64, 64, experts, top_k, E, A, 1 << 40,

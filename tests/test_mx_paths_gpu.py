@@ -288,3 +288,26 @@ def test_example_layer():
     for error, product in mx_layer.main(["--tokens", "1", "5", "24", "--dim", "512", "--ffn", "256",
                                          "--experts", "12", "--top-k", "3"]):
         assert error <= 2.0 ** -8 and product <= 2.0 ** -8
+
+
+@pytest.mark.parametrize("rows", [(1 << 22) - 1, 1 << 22, (1 << 26) + 9])
+def test_more_rows_than_a_grid(rows):
+    """Short rows beyond what one grid holds, and byte offsets beyond 32 bits:
+    every row as a call on a few rows of its own has it."""
+    K, t = 32, torch.bfloat16
+    x = torch.randn(rows, K, generator=gen("rows", rows), device=DEV, dtype=t)
+    w = torch.randn(K, generator=gen("weight"), device=DEV, dtype=t)
+    c = torch.full((rows, K), 255, device=DEV, dtype=torch.uint8)
+    s = torch.full((rows, 1), 77, device=DEV, dtype=torch.uint8)
+    picks = [(0, 64), (rows - 64, rows)]
+    picks += [(b - 64, min(b + 64, rows)) for b in range((1 << 22) - 1, rows, (1 << 22) - 1)]
+    for op in ("norm", "quantize"):
+        run = ((lambda a, n, c, s: binding.mx_rmsnorm(a, None, w, 1e-6, n, K, "fp8", None, None, c, s))
+               if op == "norm" else (lambda a, n, c, s: binding.mx_quantize(a, n, K, "fp8", c, s)))
+        c.fill_(255), s.fill_(77)
+        run(x, rows, c, s)
+        for lo, hi in picks:
+            few_c, few_s = torch.empty_like(c[lo:hi]), torch.empty_like(s[lo:hi])
+            run(x[lo:hi].contiguous(), hi - lo, few_c, few_s)
+            assert torch.equal(c[lo:hi], few_c) and torch.equal(s[lo:hi], few_s), (op, lo, hi)
+        assert not bool((s == 77).any()), op  # every row written (2^-50 is no scale of these)
