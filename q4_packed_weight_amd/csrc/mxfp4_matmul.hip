@@ -13,7 +13,11 @@ namespace {
 // tile, through a ring of S stages of its own in LDS (no barrier until the
 // end), and the waves' partial tiles are added in LDS in wave order.  Weights
 // are the A operand of the scaled instruction, tokens the B operand; nothing
-// is decoded.  Bound by the weights' bytes and the latency of the first loads.
+// is decoded.  Splitting input_dim inside the workgroup rather than over more
+// of them needs no second pass, and its loads need no registers.  Bound by the
+// weights' bytes and the latency of the first loads (one token, 4096 x 4096,
+// 8.9 MB of weights: 4.6 us, of which a launch and the first load are most; 16
+// tokens, 14336 x 4096, 31 MB: 10.4 us, 3.0 TB/s).
 // ALIGNED: rows of whole steps whose scales start at dwords; they come through
 // LDS too, four steps at a time.  Otherwise they come through registers, whose
 // wait also waits for the loads in flight.  Rows and tokens past the end read

@@ -11,8 +11,16 @@ namespace q4k {
 namespace {
 
 // BM tokens x BN weight rows per workgroup of WM x WN waves, each with
-// TM x TN tiles of 16x16; S stages of KS 128-position steps in LDS.  ALIGNED:
-// rows of whole steps whose scales start at dwords.
+// TM x TN tiles of 16x16; S stages of KS 128-position steps in LDS, loaded by
+// DMA (no registers, every wave's loads in flight across the barriers).
+// Weights are the A operand as they lie, tokens the B operand, both with their
+// scale bytes: nothing is decoded.  ALIGNED: rows of whole steps whose scales
+// start at dwords.
+// 256x256 tiles are bound by the matrix pipe and the loads from beyond the L2
+// taking turns imperfectly (8192^3: loads alone 255 us, products alone 300,
+// together 367, 3.0 PFLOP/s; 4096 tokens, 14336 x 4096: 186 us, 2.59 PFLOP/s,
+// where four rounds of tiles do not fill 256 CUs evenly); 64x64 ones by
+// the latency of their few stages (64 tokens, 14336 x 4096: 13.0 us).
 template <int AF, int T, int WM, int WN, int TM, int TN, int KS, int S, bool ALIGNED>
 __global__ __launch_bounds__(64 * WM * WN, 2) void mxfp4_tiled_kernel(
     const uint8_t *a, const uint8_t *as, const uint8_t *w, const uint8_t *ws, void *y, int M,
@@ -347,7 +355,7 @@ void launch(const uint8_t *a, const uint8_t *as, const uint8_t *w, const uint8_t
 // The tile by estimated time.  Measured at input_dim 4096, e4m3 tokens, bf16
 // outputs (graph replays, us): 64x64 tiles 11.5 up to 256 of them, 18.2 for
 // 512, 31 for 1024, 56.6 for 2048; 128x128 tiles 23.4 for 128, 25.0 for 256,
-// 39.3 for 512, 68 for 896; 256x256 tiles 44.6 for 64, 51.7 for 224, 200 for
+// 39.3 for 512, 68 for 896; 256x256 tiles 44.6 for 64, 48.7 for 224, 186 for
 // 896, a whole round of 256 at a time.  Other lengths scale all three alike.
 template <int AF, int T>
 void choose(const uint8_t *a, const uint8_t *as, const uint8_t *w, const uint8_t *ws, int M,

@@ -84,7 +84,8 @@ Workspace layout(void *base, int type, int64_t T, int64_t H, int64_t F, int64_t 
 
 // logits[t, e] for TT tokens per workgroup and one expert; the workgroups
 // also share out the splitting of x, and the down product's counters start
-// from zero here.
+// from zero here.  Bound by latency: 2.4 us for one token, 4.6 for 13 of 1056
+// on 24 experts.
 template <int TY, int TT>
 __global__ __launch_bounds__(256) void moe_router_kernel(const void *x, const void *router,
                                                          const float *bias, float *logits,
@@ -438,7 +439,10 @@ __device__ __forceinline__ int count_before(const uint32_t *row, int from, int t
 // chose it, 4 XC tokens at a time.  An expert's rank for a token is the number
 // of experts before it in the order (logit descending, index ascending), so
 // each workgroup finds its tokens by counting, without a sort; ranks below k
-// are the chosen ones and give each slot exactly one writer.
+// are the chosen ones and give each slot exactly one writer.  Bound by the
+// weights (32 tokens on 2 of 8 experts of 4096x14336: 499 MB in 116 us, 4.3
+// TB/s; a copy runs at 5.2), for one token by the router's latency before it,
+// its own prologue (about 2 us) and the first load (8.5 us, 17.8 MB).
 template <int NPX, int NPH, int NF, int XC, int W, int P, int SW, int SX, bool ALIGNED>
 __global__ __launch_bounds__(W * 64) void moe_up_kernel(UpArgs p) {
   typedef MoeRing<2, NF, XC, NPX, P, SW, SX> Ring;
@@ -583,7 +587,9 @@ struct DownArgs {
 // Output rows h0 .. h0+16 NR-1 of one expert for every token that chose it,
 // unweighted, by slot.  The workgroup that finds itself the last of its rows
 // then adds up the slots of every token, in the order of their ranks and with
-// the softmax's weights.
+// the softmax's weights: the sum has one order, and no fourth kernel is
+// needed.  Bound by the weights (as above: 249 MB in 63 us, 4.0 TB/s), for one
+// token by latency (8.6 us, 8.9 MB).
 template <int TY, int NR, int XC, int W, int P, int SW, int SX, bool ALIGNED>
 __global__ __launch_bounds__(W * 64) void moe_down_kernel(DownArgs p) {
   constexpr int NPH = kHParts<TY>;
