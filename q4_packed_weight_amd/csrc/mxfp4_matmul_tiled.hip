@@ -298,19 +298,29 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mxfp4_tiled_kernel(
       f[4 + q] = acc[i][j + 1][q];
     }
   };
-  if (TN >= 4 && wide && rows_m == BM && rows_n == BN) {
-    // Whole tiles go out through LDS, 16 tokens at a time in a part of the
-    // wave's own, so that a store covers whole cache lines of a token's row:
-    // straight from registers it covers 64 bytes of 16 rows (4096x128x16384,
-    // 134 MB of bf16 outputs: 64 us, so 48).  Past the caches, 43 us: the
-    // kernel's end does not wait for their lines to be written back.
-    constexpr int kSize = T == MX_F32 ? 4 : 2, kRow = 16 * TN * kSize, kStride = kRow + 16;
-    constexpr int kLanes = kRow / 16, kTokens = 64 / kLanes;  // of a store
-    static_assert(kW * 16 * kStride <= (int)sizeof(lds) || TN < 4, "");
+  const bool whole = TN >= 4 && wide && rows_m == BM && rows_n == BN;
+  if (whole || !wide) {
+    // Out through LDS, 16 tokens at a time in a part of the wave's own, so that
+    // a store covers whole runs of a token's row: straight from registers it
+    // covers pieces of 16 rows.  Whole tiles: 4096x128x16384, 134 MB of bf16
+    // outputs, 64 us, so 48, and past the caches 43, as the kernel's end does
+    // not wait for their lines to be written back.  Rows that do not start at
+    // 16 bytes go out value by value, 64 neighbours to a store
+    // (4096x4096x4097 bf16 110 us, so 85; 333x1056x4097 10.0, so 8.7; 16 bytes
+    // at a time between the rows' ends: 95, 10.3).
+    typedef typename MxStore<T>::type Out;
+    constexpr int kSize = sizeof(Out), kRow = 16 * TN * kSize, kStride = kRow + 16;
+    constexpr int kLanes = kRow / 16, kTokens = 64 / kLanes;  // of a store of 16 bytes a lane
+    static_assert(kW * 16 * kStride <= (int)sizeof(lds), "");
+    const int columns = rows_n - wn * 16 * TN;                // may pass the tile's, or be none
+    uint8_t *const part = lds + wave * (16 * kStride);
     lds_barrier();  // every wave's operands are read
 #pragma unroll
     for (int i = 0; i < TM; i++) {
-      uint8_t *const part = lds + wave * (16 * kStride);
+      const int first = (wm * TM + i) * 16;
+      const auto out_row = [&](int t) {
+        return static_cast<Out *>(y) + (int64_t)(m0 + first + t) * N + n0 + wn * 16 * TN;
+      };
 #pragma unroll
       for (int j = 0; j < TN; j += 2) {
         float f[8];
@@ -318,17 +328,28 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mxfp4_tiled_kernel(
         store_raw8<T>(part + r * kStride + (16 * j + 8 * g) * kSize, 0, f32_to_raw8<T>(f));
       }
       wait_lds();
+      if (TN >= 4 && wide) {
 #pragma unroll
-      for (int q = 0; q < 16 / kTokens; q++) {
-        const int t = q * kTokens + lane / kLanes, at = lane % kLanes * 16;
-        const u32x4 v = *reinterpret_cast<const u32x4 *>(part + t * kStride + at);
-        uint8_t *const row = static_cast<uint8_t *>(y) +
-                             ((int64_t)(m0 + (wm * TM + i) * 16 + t) * N + n0 + wn * 16 * TN) * kSize;
-        __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(row + at));
+        for (int q = 0; q < 16 / kTokens; q++) {
+          const int t = q * kTokens + lane / kLanes, at = lane % kLanes * 16;
+          const u32x4 v = *reinterpret_cast<const u32x4 *>(part + t * kStride + at);
+          __builtin_nontemporal_store(
+              v, reinterpret_cast<u32x4 *>(reinterpret_cast<uint8_t *>(out_row(t)) + at));
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 16 * 16 * TN; c += 64) {
+          const int t = (c + lane) / (16 * TN), at = (c + lane) % (16 * TN);
+          const Out v = *reinterpret_cast<const Out *>(part + t * kStride + at * kSize);
+          if (first + t < rows_m && at < columns) out_row(t)[at] = v;
+        }
       }
+      wait_lds();  // the part is read
     }
     return;
   }
+  // Partial tiles, and tiles whose rows are no longer than what four lanes
+  // write, of rows that start at 16 bytes.
 #pragma unroll
   for (int i = 0; i < TM; i++) {
     const int m = (wm * TM + i) * 16 + r;
@@ -338,7 +359,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mxfp4_tiled_kernel(
       const int n = (wn * TN + j) * 16 + 8 * g;
       float f[8];
       pair(i, j, f);
-      store_row8<T>(y, (int64_t)(m0 + m) * N + n0 + n, f, rows_n - n, wide);
+      store_row8<T>(y, (int64_t)(m0 + m) * N + n0 + n, f, rows_n - n, true);
     }
   }
 }
