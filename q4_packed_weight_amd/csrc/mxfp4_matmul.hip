@@ -239,9 +239,9 @@ hipError_t mxfp4_matmul_launch(const uint8_t *a, const uint8_t *as, int a_format
                                const uint8_t *w, const uint8_t *ws, int64_t M, int64_t K,
                                int64_t N, void *Y, int type, hipStream_t stream) {
   // 33 to 64 tokens: tiles of 64x64 where there are enough of them (64x14336
-  // 12.9 us, against 13.5 with 64 rows a workgroup here) or where the scales
-  // need registers (40x1056x4097 5.8 against 8.4)
-  const bool few = M <= 32 || (M <= 64 && N <= 8192 && mx_aligned_scales(as, ws, K));
+  // 12.9 us, against 13.5 with 64 rows a workgroup here; fewer: 40x1056x4097
+  // 6.4 against 5.9 here, 64x4128x4096 17.4 against 15.1)
+  const bool few = M <= 32 || (M <= 64 && N <= 8192);
   if (!few && K <= kMxTiledMaxDim)
     return mxfp4_matmul_tiled_launch(a, as, a_format, w, ws, M, K, N, Y, type, stream);
 #define CALL(AF)                                                                        \
