@@ -164,14 +164,19 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mxfp4_tiled_kernel(
                                    operand_at<MX_FP4>(r, g));
   };
   // The scales of steps s .. s+3 (a multiple of four), one to a byte; kHalves,
-  // which has no registers for four dwords a tile, keeps them so.
+  // which has no registers for four dwords a tile, keeps them so.  A stage of
+  // two steps multiplies both where the row has only the first: the second's
+  // codes are zeros, and its scales are held at 1, as the bytes behind a row's
+  // are the next row's, whose 255 would make these zeros NaN.
   const auto fetch_scales = [&](int s) {
     const uint8_t *sc = scales + (s / kChunk % 2) * kScales + s % kChunk * 4;
     const uint32_t which = byte_of_two(g);
+    const uint32_t past = KS == 1 || s + 4 <= steps ? 0u : ~0u << (8 * (steps - s));
     const auto one = [&](int row) {
       const uint8_t *p = sc + row * 4 * kChunk;
       if constexpr (kHalves) return *reinterpret_cast<const int *>(p + 4 * g);
-      else return (int)byte_of_four(*reinterpret_cast<const u32x4 *>(p), which);
+      const uint32_t v = byte_of_four(*reinterpret_cast<const u32x4 *>(p), which);
+      return (int)((v & ~past) | (0x7F7F7F7Fu & past));
     };
 #pragma unroll
     for (int i = 0; i < TM; i++) sa[i] = one((wm * TM + i) * 16 + r);
