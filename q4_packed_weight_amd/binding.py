@@ -110,13 +110,18 @@ def _ptr(t):
 
 
 # The current stream's handle without a Stream object around it, which takes
-# longer to make than everything else here.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# longer to make than everything else here; a torch built without a GPU lacks
+# these names, and its public call says so.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _stream(stream):
-    return _raw_stream(_current_device()) if stream is None else stream.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None or _current_device is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(_current_device())
 
 
 def _check(rc, func):
