@@ -91,11 +91,13 @@ int mx_rmsnorm(const void *x, const void *residual, const void *weight, float ep
 /*
  * mxfp4_matmul -- Y[t, o] = sum_k A[t, k] * W[o, k], t < n_tokens, with W in
  * MXFP4 and A in MXFP8 or MXFP4, as gfx950's scaled matrix instructions
- * multiply them; accumulated in fp32 and rounded once to y_type.  MXFP8
- * activations with fp32 outputs take two instructions for each product, as
- * one alone adds e4m3 products with an error of up to 2^-11 of the largest of
- * 128 (about 5e-6 of a result's norm on normal data), which 16-bit outputs
- * do not show.
+ * multiply them; accumulated in fp32 and rounded once to y_type.  One such
+ * instruction adds 128 e4m3 products with an error of up to 2^-11 of the
+ * largest of them (about 5e-6 of a result's norm on normal data).  With fp32
+ * outputs MXFP8 activations take two instructions for each product, without
+ * that error; with 16-bit outputs they take one.  The error is then below half
+ * a step of most outputs, but not of one whose products cancel: take fp32
+ * outputs where that matters.  MXFP4 activations have none of it.
  *   a_codes, a_scales  n_tokens rows of input_dim values in a_format
  *   w_codes, w_scales  output_dim rows of input_dim values in MX_FP4
  *   codes 16-byte aligned, scales any alignment
@@ -127,10 +129,23 @@ int mxfp4_matmul(const uint8_t *a_codes, const uint8_t *a_scales, int a_format,
  *   workspace  mxfp4_moe_workspace_size bytes, 256-byte aligned, of any
  *              content; its content after the call is undefined.  Calls that
  *              share one must not overlap in time.
- * e2m1 weights times their block's scale are exact in bf16; activations enter
- * as one (bf16), two (fp16) or three (fp32) bf16 values and h as two, or three
- * for fp32, so only fp32-level rounding lies between x and y (x below 2^127).
- * At most 64 tokens run at a time, more loop over them; fewer from 129 experts
+ * What lies between x and y, for finite x and h below 2^127:
+ *   logits  fp32 sums, off by up to (input_dim / 256 + 24) 2^-23 of the sum of
+ *           |x| |router| and |bias|; of experts whose logits lie closer, either
+ *           may be chosen
+ *   x       enters the products as one (bf16), two (fp16) or three (fp32) bf16
+ *           values that add up to it
+ *   h       enters as three bf16 values for fp32, which add up to it, and as
+ *           two for bf16 and fp16, off by up to 2^-17 of each |h| before the
+ *           sum over ffn_dim
+ *   weights e2m1 times their block's scale, exact in bf16 for scale bytes up to
+ *           252, as mx_quantize makes them (253: 4 and 6 are infinite, 254: 2
+ *           and above); 255 makes the outputs that use the block NaN
+ *   sums    fp32
+ * An expert's weights are read once for up to 16 of its tokens (8 where
+ * n_tokens * top_k is at most 2 * n_experts), and again for more.  At most 64
+ * tokens run at a time, more loop over them and read the experts' weights
+ * again: the call is for few tokens.  Fewer run at a time from 129 experts
  * on (8192 / n_experts), and where top_k * max(input_dim, ffn_dim) passes 5.5
  * million (2^31 / 6 of it, so that a group's slots stay within 31-bit offsets).
  * workspace_bytes too small gives Q4K_ESCRATCH.
