@@ -240,7 +240,8 @@ hipError_t mxfp4_matmul_launch(const uint8_t *a, const uint8_t *as, int a_format
                                int64_t N, void *Y, int type, hipStream_t stream) {
   // 33 to 64 tokens: tiles of 64x64 where there are enough of them (64x14336
   // 12.9 us, against 13.5 with 64 rows a workgroup here; fewer: 40x1056x4097
-  // 6.4 against 5.9 here, 64x4128x4096 17.4 against 15.1)
+  // 6.4 against 5.9 here, 64x4128x4096 17.4 against 15.1, at the border
+  // 64x4128x8192 17.7 against 18.2)
   const bool few = M <= 32 || (M <= 64 && N <= 8192);
   if (!few && K <= kMxTiledMaxDim)
     return mxfp4_matmul_tiled_launch(a, as, a_format, w, ws, M, K, N, Y, type, stream);

@@ -18,8 +18,9 @@ namespace {
 // start at dwords.
 // 256x256 tiles are bound by the matrix pipe and the loads from beyond the L2
 // taking turns imperfectly (8192^3: loads alone 255 us, products alone 300,
-// together 367, 3.0 PFLOP/s; 4096 tokens, 14336 x 4096: 186 us, 2.59 PFLOP/s,
-// where four rounds of tiles do not fill 256 CUs evenly); 64x64 ones by
+// together 367, 3.0 PFLOP/s; 4096 tokens, 14336 x 4096: 182 us, 2.64 PFLOP/s,
+// where four rounds of tiles do not fill 256 CUs evenly; fp32 outputs, two
+// instructions a product, 347 us); 64x64 ones by
 // the latency of their few stages (64 tokens, 14336 x 4096: 13.0 us).
 template <int AF, int T, int WM, int WN, int TM, int TN, int KS, int S, bool ALIGNED>
 __global__ __launch_bounds__(64 * WM * WN, 2) void mxfp4_tiled_kernel(
@@ -309,7 +310,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mxfp4_tiled_kernel(
     // a store covers whole runs of a token's row: straight from registers it
     // covers pieces of 16 rows.  Whole tiles: 4096x128x16384, 134 MB of bf16
     // outputs, 64 us, so 48, and past the caches 43, as the kernel's end does
-    // not wait for their lines to be written back.  Rows that do not start at
+    // not wait for their lines to be written back; smaller outputs go the same
+    // way, which is not timed apart.  Rows that do not start at
     // 16 bytes go out value by value, 64 neighbours to a store
     // (4096x4096x4097 bf16 110 us, so 85; 333x1056x4097 10.0, so 8.7; 16 bytes
     // at a time between the rows' ends: 95, 10.3).
@@ -382,7 +384,9 @@ void launch(const uint8_t *a, const uint8_t *as, const uint8_t *w, const uint8_t
 // outputs (graph replays, us): 64x64 tiles 11.5 up to 256 of them, 18.2 for
 // 512, 31 for 1024, 56.6 for 2048; 128x128 tiles 23.4 for 128, 25.0 for 256,
 // 39.3 for 512, 68 for 896; 256x256 tiles 44.6 for 64, 48.7 for 224, 186 for
-// 896, a whole round of 256 at a time.  Other lengths scale all three alike.
+// 896, a whole round of 256 at a time.  Other lengths and formats, and fp32
+// outputs, whose products take twice as long, are taken to scale all three
+// alike; that is not measured.
 template <int AF, int T>
 void choose(const uint8_t *a, const uint8_t *as, const uint8_t *w, const uint8_t *ws, int M,
             int64_t K, int64_t N, void *Y, hipStream_t stream) {

@@ -3,8 +3,11 @@
 // with the activation between them, and the down product with the sum over
 // the chosen experts.
 //
-// The weights are read once per call and everything else is small, so the
-// layer is bound by the weight stream.  e2m1 codes times their block's power
+// An expert's weights are read once for up to 16 of its tokens, again for the
+// next ones, and again for each 64 tokens of the call; everything else is
+// small, so for few tokens the layer is bound by the weight stream (2 of 8
+// experts of 4096x14336 bf16: 32 tokens 192 us; 64 tokens, about 1.4 passes,
+// 290; 256 tokens 1142, 1024 tokens 4641).  e2m1 codes times their block's power
 // of two are exact bf16 values, made by one conversion instruction a pair,
 // and run on the 16x16x32 bf16 matrix instruction as its A operand (16 rows);
 // tokens are the columns.  Activations that bf16 cannot hold enter as the sum
@@ -708,7 +711,10 @@ hipError_t launch(const MoeArgs &a, const Workspace &w, hipStream_t stream) {
                    a.y, a.T, a.H, a.F, a.E, a.k};
   // Wide tiles read the activations less often, narrow ones make more
   // workgroups: the widest that make 512, two for each CU, whose rings fit the
-  // CU's LDS twice at least.
+  // CU's LDS twice at least.  The up kernel's keys are not counted: from 54
+  // tokens on 128 experts, or 28 on 256, they leave room for one workgroup of
+  // the widest bf16 tiles (64 tokens on 8 of 128 experts of 2048x768: 174 us,
+  // its weights at the streaming rate 55).
   const auto tiles = [](int rows, int n) { return (rows + 16 * n - 1) / (16 * n); };
   const auto run = [&](auto xc) {
     constexpr int XC = decltype(xc)::value;
