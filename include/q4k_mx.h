@@ -1,7 +1,8 @@
 /*
  * q4k_mx.h -- microscaled (MX) operators of libq4k.so: quantisation to and
  * from MXFP4 / MXFP8, the root-mean-square norm that feeds them, the product
- * with MXFP4 weights, and a mixture-of-experts layer of such weights.
+ * with MXFP4 weights, a mixture-of-experts layer of such weights, and attention
+ * over keys and values cached in these formats, with rotary positions.
  *
  * The contract of q4k.h holds here too: device pointers owned by the caller,
  * validation before anything is launched (dimensions, types and formats,
@@ -157,6 +158,155 @@ int mxfp4_moe(const void *x, int type, const void *router, const float *router_b
               const uint8_t *down_scales, int64_t n_tokens, int64_t input_dim, int64_t ffn_dim,
               int64_t n_experts, int64_t top_k, void *y, void *workspace, int64_t workspace_bytes,
               void *stream);
+
+/*
+ * Attention over a quantised cache.  mx_rotary turns a step's queries and
+ * keys, mx_cache_write stores its keys and values, mx_attention lets the
+ * queries see them; mx_cache_read takes rows out again.
+ *
+ * The cache is a pool of pages, each of page_size tokens, in four arrays in
+ * the MX format above (rows are a head's values, without padding):
+ *   k_codes, v_codes    [n_pages][n_heads][page_size][head_dim (MX_FP8) or
+ *                       head_dim/2 (MX_FP4)] bytes, 16-byte aligned
+ *   k_scales, v_scales  [n_pages][n_heads][page_size][head_dim/32] bytes
+ * A token's slot is page * page_size + its place in the page.
+ *   page_size  1 .. 65536; n_pages > 0; n_pages * page_size below 2^31
+ *   head_dim   a multiple of 32, at most 256
+ * Rows of values have strides: row t of x is at x + t * x_stride values, its
+ * heads one after the other from there; at least n_heads * head_dim, and so
+ * that every row starts at a multiple of 16 bytes.
+ * These calls take no state from one to the next and may run at once with
+ * others, as long as none writes what another reads or writes.
+ */
+
+/* Layouts of a rotary pair. */
+#define MX_ROTARY_HALF 0        /* values i and i + rotary_dim/2 */
+#define MX_ROTARY_INTERLEAVED 1 /* values 2i and 2i + 1 */
+
+/* Frequencies for contexts longer than the trained ones. */
+#define MX_ROTARY_NONE 0
+#define MX_ROTARY_LINEAR 1
+#define MX_ROTARY_NTK 2
+#define MX_ROTARY_YARN 3
+#define MX_ROTARY_BANDS 4
+
+/*
+ * mx_rotary -- the first rotary_dim values of each head as pairs (a, b), each
+ * turned by its angle w = positions[t] * frequencies[i], i < rotary_dim/2:
+ *   (a cos w - b sin w, b cos w + a sin w) * amplitude
+ * and the others as they are.
+ *   x, y        [n_tokens] rows of n_heads heads of `type`, 16-byte aligned;
+ *               y may be x (of the same stride): what is not turned then stays
+ *               unread
+ *   positions   [n_tokens], any values below 2^53
+ *   frequencies fp64 [rotary_dim/2], radians a position
+ *   n_heads 1 .. 4096; head_dim a multiple of 8, at most 512; rotary_dim even,
+ *   2 .. head_dim; n_tokens > 0, below 2^31
+ * The angle is made in fp64 and reduced to half a turn there; its cosine and
+ * sine, the products and their sum are fp32, rounded once to `type`.
+ */
+int mx_rotary(const void *x, int64_t x_stride, int type, const int64_t *positions,
+              const double *frequencies, float amplitude, int64_t n_tokens, int64_t n_heads,
+              int64_t head_dim, int64_t rotary_dim, int layout, void *y, int64_t y_stride,
+              void *stream);
+
+/*
+ * mx_rotary_frequencies -- a table for mx_rotary, on the host: with
+ * f = base^(-2i / rotary_dim), i < rotary_dim/2,
+ *   NONE    f
+ *   LINEAR  f / factor
+ *   NTK     f for the base base * factor^(rotary_dim / (rotary_dim - 2))
+ *   YARN    between f / factor and f: f's share falls from 1 to 0 over the
+ *           indices from that of the pair with `high` turns over `trained`
+ *           positions to that of the one with `low` (YaRN, Peng et al. 2023);
+ *           *amplitude = 0.1 ln(factor) + 1
+ *   BANDS   between them too: f's share is (turns - low) / (high - low), held
+ *           to 0 .. 1, for the turns that f makes over `trained` positions
+ * and *amplitude = 1 but for YARN.
+ *   frequencies, amplitude  HOST pointers, fp64 [rotary_dim/2] and [1]
+ *   rotary_dim  even, 2 .. 512; base > 1; factor >= 1 but for NONE;
+ *               0 < low < high and trained >= 1 for YARN and BANDS; all finite
+ */
+int mx_rotary_frequencies(int64_t rotary_dim, double base, int scaling, double factor,
+                          double trained, double low, double high, double *frequencies,
+                          double *amplitude);
+
+/*
+ * mx_cache_write -- rows of keys and values as the blocks of their slots, as
+ * mx_quantize makes them.
+ *   k, v       [n_tokens] rows of n_heads heads of `type`, 16-byte aligned
+ *   slots      [n_tokens], each at most once; a slot outside the cache (-1)
+ *              leaves its token out
+ *   n_tokens > 0, below 2^31; n_heads 1 .. 4096
+ */
+int mx_cache_write(const void *k, int64_t k_stride, const void *v, int64_t v_stride, int type,
+                   const int64_t *slots, int64_t n_tokens, int64_t n_heads, int64_t head_dim,
+                   int format, uint8_t *k_codes, uint8_t *k_scales, uint8_t *v_codes,
+                   uint8_t *v_scales, int64_t n_pages, int64_t page_size, void *stream);
+
+/*
+ * mx_cache_read -- the values of slots, rounded to `type` as mx_dequantize
+ * does.
+ *   slots      [n_tokens], in any order, also more than once; one outside the
+ *              cache reads as zeros
+ *   k, v       as in mx_cache_write, written
+ */
+int mx_cache_read(const int64_t *slots, int64_t n_tokens, int64_t n_heads, int64_t head_dim,
+                  int format, const uint8_t *k_codes, const uint8_t *k_scales,
+                  const uint8_t *v_codes, const uint8_t *v_scales, int64_t n_pages,
+                  int64_t page_size, void *k, int64_t k_stride, void *v, int64_t v_stride,
+                  int type, void *stream);
+
+/*
+ * mx_attention -- for token i of sequence s and head h, over the keys j of the
+ * sequence that the token sees,
+ *   y = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale * q . k_j)
+ * with the key head h / (n_heads / n_kv_heads).
+ *   q, y       [n_tokens] rows of n_heads heads of `type`, 16-byte aligned
+ *   query_starts  [n_seqs + 1]: sequence s has the tokens query_starts[s] up
+ *              to query_starts[s+1], ascending; tokens of none of them are
+ *              left as they were in y
+ *   key_counts [n_seqs]: keys of each sequence, its new tokens' among them; 0
+ *              is allowed, more than its pages hold count as so many
+ *   pages      [n_seqs][pages_per_seq]: its pages in order; an entry outside
+ *              0 .. n_pages-1 is a page of no keys
+ *   max_queries  no sequence has more tokens (further ones are left as they
+ *              were)
+ *   causal     not 0: a sequence's last token sees all of its keys, the one
+ *              before it all but the last, and so on (none at all where it has
+ *              more tokens than keys); 0: every token sees all
+ *   window     > 0: only the last `window` of those; 0: all (causal only)
+ * A token that sees nothing gives zeros.  What it does not see has no influence,
+ * NaN and unwritten pages too; a NaN block of a key that it sees makes its y NaN,
+ * one of a value the 32 values of y that use it.
+ *   n_heads    a multiple of n_kv_heads, at most 4096
+ *   n_tokens > 0, below 2^31; n_seqs, max_queries, pages_per_seq > 0;
+ *   pages_per_seq * page_size below 2^30; n_seqs * n_kv_heads *
+ *   ceil(max_queries * n_heads / n_kv_heads / 16) below 2^24; scale finite
+ *   workspace  mx_attention_workspace_size bytes (NULL if 0), 256-byte
+ *              aligned, of any content; its content after the call is
+ *              undefined.  Calls that share one must not overlap in time.
+ * What lies between q and y (fp16 operands with powers of two taken out, fp32
+ * sums):
+ *   q          exact for bf16 and fp16; fp32 as two fp16 values, off by 2^-23
+ *              of each; below 2^-29 of a row's largest bits are lost
+ *   k, v       exact where the scale bytes of the keys taken together (32 or
+ *              64 in a row) lie within 21 (MX_FP8) or 36 (MX_FP4) of their
+ *              largest, values above 2^-55; lower ones lose bits
+ *   w          off by 2^-11 of each (bf16 and fp16), 2^-23 (fp32)
+ * The order of the sums depends on the sizes, starts and counts alone.
+ */
+int64_t mx_attention_workspace_size(int64_t n_tokens, int64_t n_heads, int64_t n_kv_heads,
+                                    int64_t head_dim, int64_t n_seqs, int64_t pages_per_seq,
+                                    int64_t page_size, int64_t max_queries);
+int mx_attention(const void *q, int64_t q_stride, int type, const int32_t *query_starts,
+                 const int32_t *key_counts, const int32_t *pages, int64_t n_tokens,
+                 int64_t n_heads, int64_t n_kv_heads, int64_t head_dim, int64_t n_seqs,
+                 int64_t pages_per_seq, int64_t max_queries, float scale, int causal,
+                 int64_t window, int format, const uint8_t *k_codes, const uint8_t *k_scales,
+                 const uint8_t *v_codes, const uint8_t *v_scales, int64_t n_pages,
+                 int64_t page_size, void *y, int64_t y_stride, void *workspace,
+                 int64_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

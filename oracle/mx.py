@@ -132,3 +132,61 @@ def moe(x, router, bias, up, down, k, parts_error):
         if near:
             err[t] = np.inf
     return y, err
+
+
+def rotary(x, positions, frequencies, amplitude, rotary_dim, layout):
+    """x [tokens][heads][head_dim]."""
+    y = np.array(x, np.float64)
+    w = np.asarray(positions, np.float64)[:, None] * np.asarray(frequencies, np.float64)
+    c, s = (amplitude * np.cos(w))[:, None], (amplitude * np.sin(w))[:, None]
+    h = rotary_dim // 2
+    one = slice(0, h) if layout == "half" else slice(0, rotary_dim, 2)
+    two = slice(h, rotary_dim) if layout == "half" else slice(1, rotary_dim, 2)
+    a, b = y[..., one].copy(), y[..., two].copy()
+    y[..., one], y[..., two] = a * c - b * s, b * c + a * s
+    return y
+
+
+def rotary_frequencies(d, base, scaling="none", factor=1.0, trained=8192.0, low=1.0, high=32.0):
+    """(frequencies, amplitude), pair by pair from the definitions."""
+    if scaling == "ntk" and d > 2:
+        base = base * factor ** (d / (d - 2))
+    f = np.array([base ** (-2 * i / d) for i in range(d // 2)])
+    turns = trained * f / (2 * np.pi)
+    if scaling == "linear":
+        return f / factor, 1.0
+    if scaling == "bands":
+        keep = np.clip((turns - low) / (high - low), 0, 1)
+        return f * keep + f / factor * (1 - keep), 1.0
+    if scaling == "yarn":
+        # turns(i) = trained / (2 pi base^(2i/d)) solved for i
+        at = [d / 2 * np.log(trained / (2 * np.pi * n)) / np.log(base) for n in (high, low)]
+        first, last = max(np.floor(at[0]), 0), min(np.ceil(at[1]), d - 1)
+        keep = 1 - np.clip((np.arange(d // 2) - first) / max(last - first, 1e-3), 0, 1)
+        return f * keep + f / factor * (1 - keep), 0.1 * np.log(factor) + 1
+    return f, 1.0
+
+
+def attention(q, k, v, scale, sees):
+    """Rows of q [rows][dim] over keys and values [keys][dim]; sees [rows][keys].
+    (y, sum of the weights' shares of |v|, largest score seen, largest sum of
+    |q||k| seen)."""
+    q, k, v = (np.asarray(a, np.float64) for a in (q, k, v))
+    rows, dim = q.shape
+    y, mass = np.zeros((rows, dim)), np.zeros((rows, dim))
+    top, size = np.zeros(rows), np.zeros(rows)
+    for r in range(rows):
+        j = np.nonzero(sees[r])[0]
+        if not len(j):
+            continue
+        x = (k[j] @ q[r]) * scale
+        if np.isnan(x).any():
+            y[r] = np.nan
+            continue
+        w = np.exp(x - x.max())
+        w /= w.sum()
+        y[r] = w @ v[j]
+        mass[r] = w @ np.abs(v[j])
+        top[r] = np.abs(x).max()
+        size[r] = (np.abs(k[j]) @ np.abs(q[r])).max() * abs(scale)
+    return y, mass, top, size

@@ -25,6 +25,8 @@ Q4K_EINVAL_TYPE = -6
 # Value types and block formats of the MX operators (include/q4k_mx.h).
 MX_TYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 MX_FORMAT = {"fp4": 4, "fp8": 8}
+ROTARY_LAYOUT = {"half": 0, "interleaved": 1}
+ROTARY_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
 
 EXPORTED = (
     "q4k_gemv", "q4k_matmul", "ternary_gemv_codes", "ternary_gemv", "ternary_matmul",
@@ -36,6 +38,8 @@ EXPORTED = (
     "q4k_strerror",
     "mx_quantize", "mx_dequantize", "mx_rmsnorm", "mxfp4_matmul", "mxfp4_moe_workspace_size",
     "mxfp4_moe",
+    "mx_rotary", "mx_rotary_frequencies", "mx_cache_write", "mx_cache_read",
+    "mx_attention_workspace_size", "mx_attention",
     "q4k_bench_empty", "q4k_bench_delay", "q4k_bench_stream_read", "q4k_bench_copy",
 )
 
@@ -61,6 +65,7 @@ def lib():
             "(there is no fallback implementation)")
     L = ctypes.CDLL(LIB_PATH)
     P, I64, I, F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
+    DBL = ctypes.c_double
     sig = {
         "q4k_gemv": [P, P, I64, I64, P, P],
         "q4k_matmul": [P, P, I64, I64, I64, P, P],
@@ -86,6 +91,12 @@ def lib():
         "mx_rmsnorm": [P, P, P, F, I, I64, I64, P, P, I, P, P, P],
         "mxfp4_matmul": [P, P, I, P, P, I64, I64, I64, P, I, P],
         "mxfp4_moe": [P, I, P, P, P, P, P, P, I64, I64, I64, I64, I64, P, P, I64, P],
+        "mx_rotary": [P, I64, I, P, P, F, I64, I64, I64, I64, I, P, I64, P],
+        "mx_rotary_frequencies": [I64, DBL, I, DBL, DBL, DBL, DBL, P, P],
+        "mx_cache_write": [P, I64, P, I64, I, P, I64, I64, I64, I, P, P, P, P, I64, I64, P],
+        "mx_cache_read": [P, I64, I64, I64, I, P, P, P, P, I64, I64, P, I64, P, I64, I, P],
+        "mx_attention": [P, I64, I, P, P, P, I64, I64, I64, I64, I64, I64, I64, F, I, I64, I, P, P,
+                         P, P, I64, I64, P, I64, P, I64, P],
         "q4k_bench_empty": [P],
         "q4k_bench_delay": [I64, P],
         "q4k_bench_stream_read": [P, I64, P, I64, P],
@@ -99,6 +110,8 @@ def lib():
     L.q4k_tiled_size.restype = I64
     L.mxfp4_moe_workspace_size.argtypes = [I64, I64, I64, I64, I64]
     L.mxfp4_moe_workspace_size.restype = I64
+    L.mx_attention_workspace_size.argtypes = [I64] * 8
+    L.mx_attention_workspace_size.restype = I64
     L.q4k_strerror.argtypes = [I]
     L.q4k_strerror.restype = ctypes.c_char_p
     _lib = L
@@ -491,6 +504,134 @@ def mxfp4_moe(x, router, router_bias, up_codes, up_scales, down_codes, down_scal
                          _arg(y, d, "y", n), _arg(workspace, u8, "workspace", 0),
                          0 if workspace is None else workspace.numel(), _stream(stream))
     _check(rc, "mxfp4_moe")
+    return y
+
+
+def _choice(table, key, name):
+    code = table.get(key)
+    if code is None:
+        raise ValueError(f"{name} must be one of {', '.join(table)}, got {key!r}")
+    return code
+
+
+def _rows(t, dtype, name, rows, heads, head_dim):
+    """(pointer, values from a row to the next) of [rows][heads * head_dim] or
+    [rows][heads][head_dim] values; rows may lie apart, as slices of a wider
+    matrix do."""
+    if t is None:
+        return None, heads * head_dim
+    width = heads * head_dim
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if _current_device is not None and t.device.index != _current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is another")
+    shape, stride = tuple(t.shape), t.stride()
+    if rows <= 0 or width <= 0:  # refused by the C side
+        return t.data_ptr(), width
+    if shape == (rows, width):
+        whole = width == 1 or stride[1] == 1
+    elif shape == (rows, heads, head_dim):
+        whole = (head_dim == 1 or stride[2] == 1) and (heads == 1 or stride[1] == head_dim)
+    else:
+        raise ValueError(f"{name} must be [{rows}][{width}] or [{rows}][{heads}][{head_dim}], "
+                         f"got {list(shape)}")
+    if not whole:
+        raise ValueError(f"{name}: a row's values must lie one after the other")
+    return t.data_ptr(), stride[0] if rows > 1 else width
+
+
+def mx_rotary(x, positions, frequencies, amplitude, n_tokens, n_heads, head_dim, rotary_dim,
+              layout, y, stream=None):
+    """Rotary positions; layout is "half" or "interleaved", y may be x."""
+    T, H, D, R = int(n_tokens), int(n_heads), int(head_dim), int(rotary_dim)
+    t, lay = _mx_type(x, "x"), _choice(ROTARY_LAYOUT, layout, "layout")
+    xp, xs = _rows(x, x.dtype, "x", T, H, D)
+    yp, ys = _rows(y, x.dtype, "y", T, H, D)
+    rc = lib().mx_rotary(xp, xs, t, _arg(positions, torch.int64, "positions", max(T, 0)),
+                         _arg(frequencies, torch.float64, "frequencies", max(R // 2, 0)),
+                         float(amplitude), T, H, D, R, lay, yp, ys, _stream(stream))
+    _check(rc, "mx_rotary")
+    return y
+
+
+def mx_rotary_frequencies(rotary_dim, base=10000.0, scaling="none", factor=1.0, trained=8192.0,
+                          low=1.0, high=32.0):
+    """(fp64 tensor on the host of rotary_dim / 2 frequencies, amplitude); the
+    scaling is "none", "linear", "ntk", "yarn" or "bands"."""
+    n = int(rotary_dim)
+    f = torch.zeros(max(n // 2, 1), dtype=torch.float64)
+    amplitude = ctypes.c_double(1.0)
+    rc = lib().mx_rotary_frequencies(n, float(base), _choice(ROTARY_SCALING, scaling, "scaling"),
+                                     float(factor), float(trained), float(low), float(high),
+                                     f.data_ptr(), ctypes.addressof(amplitude))
+    _check(rc, "mx_rotary_frequencies")
+    return f, amplitude.value
+
+
+def _pool(k_codes, k_scales, v_codes, v_scales, n_pages, page_size, heads, head_dim, f):
+    n = _mx_need(n_pages * heads * page_size, head_dim) if heads > 0 and page_size > 0 else 0
+    return [_arg(t, torch.uint8, name, need) for t, name, need in (
+        (k_codes, "k_codes", n * f // 8), (k_scales, "k_scales", n // 32),
+        (v_codes, "v_codes", n * f // 8), (v_scales, "v_scales", n // 32))]
+
+
+def mx_cache_write(k, v, slots, n_tokens, n_heads, head_dim, fmt, k_codes, k_scales, v_codes,
+                   v_scales, n_pages, page_size, stream=None):
+    """Rows of keys and values to the blocks of their slots; -1 leaves a token out."""
+    T, H, D, N, B = int(n_tokens), int(n_heads), int(head_dim), int(n_pages), int(page_size)
+    t, f = _mx_type(k, "k"), _mx_format(fmt)
+    kp, ks = _rows(k, k.dtype, "k", T, H, D)
+    vp, vs = _rows(v, k.dtype, "v", T, H, D)
+    rc = lib().mx_cache_write(kp, ks, vp, vs, t, _arg(slots, torch.int64, "slots", max(T, 0)), T, H,
+                              D, f, *_pool(k_codes, k_scales, v_codes, v_scales, N, B, H, D, f), N,
+                              B, _stream(stream))
+    _check(rc, "mx_cache_write")
+
+
+def mx_cache_read(slots, n_tokens, n_heads, head_dim, fmt, k_codes, k_scales, v_codes, v_scales,
+                  n_pages, page_size, k, v, stream=None):
+    """The values of slots, rounded to k's and v's type; -1 reads as zeros."""
+    T, H, D, N, B = int(n_tokens), int(n_heads), int(head_dim), int(n_pages), int(page_size)
+    t, f = _mx_type(k, "k"), _mx_format(fmt)
+    kp, ks = _rows(k, k.dtype, "k", T, H, D)
+    vp, vs = _rows(v, k.dtype, "v", T, H, D)
+    rc = lib().mx_cache_read(_arg(slots, torch.int64, "slots", max(T, 0)), T, H, D, f,
+                             *_pool(k_codes, k_scales, v_codes, v_scales, N, B, H, D, f), N, B, kp,
+                             ks, vp, vs, t, _stream(stream))
+    _check(rc, "mx_cache_read")
+    return k, v
+
+
+def mx_attention_workspace_size(n_tokens, n_heads, n_kv_heads, head_dim, n_seqs, pages_per_seq,
+                                page_size, max_queries):
+    """Bytes of mx_attention's workspace (raises on invalid dimensions)."""
+    n = lib().mx_attention_workspace_size(int(n_tokens), int(n_heads), int(n_kv_heads),
+                                          int(head_dim), int(n_seqs), int(pages_per_seq),
+                                          int(page_size), int(max_queries))
+    _check(n if n < 0 else Q4K_OK, "mx_attention_workspace_size")
+    return n
+
+
+def mx_attention(q, query_starts, key_counts, pages, n_tokens, n_heads, n_kv_heads, head_dim,
+                 n_seqs, pages_per_seq, max_queries, scale, causal, window, fmt, k_codes, k_scales,
+                 v_codes, v_scales, n_pages, page_size, y, workspace, stream=None):
+    """Attention of sequences' new tokens over their cached keys and values;
+    workspace may be None where mx_attention_workspace_size gives 0."""
+    T, H, HK, D = int(n_tokens), int(n_heads), int(n_kv_heads), int(head_dim)
+    S, P, N, B = int(n_seqs), int(pages_per_seq), int(n_pages), int(page_size)
+    t, f, i32 = _mx_type(q, "q"), _mx_format(fmt), torch.int32
+    qp, qs = _rows(q, q.dtype, "q", T, H, D)
+    yp, ys = _rows(y, q.dtype, "y", T, H, D)
+    rc = lib().mx_attention(qp, qs, t, _arg(query_starts, i32, "query_starts", max(S + 1, 0)),
+                            _arg(key_counts, i32, "key_counts", max(S, 0)),
+                            _arg(pages, i32, "pages", max(S, 0) * max(P, 0)), T, H, HK, D, S, P,
+                            int(max_queries), float(scale), int(bool(causal)), int(window), f,
+                            *_pool(k_codes, k_scales, v_codes, v_scales, N, B, HK, D, f), N, B, yp,
+                            ys, _arg(workspace, torch.uint8, "workspace", 0),
+                            0 if workspace is None else workspace.numel(), _stream(stream))
+    _check(rc, "mx_attention")
     return y
 
 

@@ -1,0 +1,243 @@
+// mx_attention.h -- what the attention kernels share: a sequence's rows and
+// the keys they see, the fp16 operands made of queries and of cached blocks,
+// and the joining of partial results.
+//
+// Operands.  Everything is multiplied in fp16 with powers of two taken out:
+//   queries  q = 2^e (h + l): e by row, so that the row's largest value lies in
+//            [2^14, 2^15); h alone holds bf16 and fp16 values, of fp32 h is
+//            rounded to fp16 and l what is left, rounded too (off by 2^-23 of
+//            the value).  What lies 2^-29 below the row's
+//            largest is lost bit by bit.
+//   keys and values  code * 2^(s - ref), ref the largest scale byte among the
+//            keys taken together, so that the largest code still fits: exact
+//            for blocks whose scale lies up to 2^21 (MX_FP8) or 2^36 (MX_FP4)
+//            below it, as fp16's subnormals reach, and these operands keep them.
+//   weights  p = exp2(x - largest x + 10), in (0, 2^10]: one fp16, off by 2^-11
+//            of p, an eighth of what bf16 would leave of it; for fp32 a second
+//            one for what is left (2^-23).  The sums of p are of the unrounded
+//            ones, in fp32.
+// Keys that some rows see and others do not (a causal chunk's own, a window's
+// edge) are taken without a common reference, which a key that a row does not
+// see would give it: each key's own for its scores, and bf16 for its values,
+// with one bf16 weight more.
+// A NaN block's scale is NaN and so are its products; a row of q that is not
+// finite has a NaN scale.
+#pragma once
+
+#include "mx_common.h"
+#include "mx_internal.h"
+
+namespace q4k {
+
+typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+
+constexpr float kMinusInf = -__builtin_inff();
+constexpr int kWeightExponent = 10;
+// The power that the largest code takes within fp16: 448 * 2^6, 6 * 2^13.
+template <int FMT> constexpr int kCodeExponent = FMT == MX_FP8 ? 6 : 13;
+
+// Keys lo .. hi (none where hi < lo).
+struct Range { int lo, hi; };
+
+struct Sequence {
+  int q0, nq, total, nk;  // first token, rows' tokens, all of its tokens, keys
+  __device__ __forceinline__ Range sees(const AttentionArgs &a, int i) const {
+    const int hi = a.causal ? nk - total + i : nk - 1;
+    return {a.window ? max(0, hi - a.window + 1) : 0, hi};
+  }
+};
+
+// Starts and counts as they should be, whatever they hold.
+__device__ __forceinline__ Sequence sequence_of(const AttentionArgs &a, int s) {
+  Sequence r;
+  r.q0 = min(max(a.starts[s], 0), a.n_tokens);
+  r.total = min(max(a.starts[s + 1], r.q0), a.n_tokens) - r.q0;
+  r.nq = min(r.total, a.max_queries);
+  r.nk = min(max(a.counts[s], 0), a.pages_per_seq * a.page_size);
+  return r;
+}
+
+// 32 keys make a step; each range of keys has at least kMinSteps of them.
+constexpr int kStepKeys = 32;
+constexpr int kMinSteps = 8;
+
+// What one workgroup works on: rows r0 .. of a sequence's (token, head of the
+// group) pairs and the steps of keys that any of them sees, or its share.
+struct Work {
+  Sequence seq;
+  int index, kv_head, r0, rows, split, splits;  // index of the sequence; splits: ranges in use
+  Range any, all;  // keys that one row at least sees, that all do
+  int begin, first, last;  // key of step 0; this share's steps
+};
+
+template <int ROWS>
+__device__ __forceinline__ bool work_of(const AttentionArgs &a, uint32_t block, int splits, Work &w) {
+  uint32_t n = a.by_kv_heads.of(block);
+  w.kv_head = block - n * a.n_kv_heads;
+  const uint32_t n2 = splits > 1 ? a.by_splits.of(n) : n;
+  w.split = n - n2 * splits;
+  const uint32_t s = a.by_tiles.of(n2);
+  w.index = s;
+  w.r0 = (n2 - s * a.tiles) * ROWS;
+  w.seq = sequence_of(a, s);
+  const int all_rows = w.seq.nq * a.group;
+  if (w.r0 >= all_rows) return false;
+  w.rows = min(ROWS, all_rows - w.r0);
+  const Range one = w.seq.sees(a, a.by_group.of(w.r0));
+  const Range two = w.seq.sees(a, a.by_group.of(w.r0 + w.rows - 1));
+  w.any = {one.lo, two.hi};
+  w.all = {two.lo, one.hi};
+  w.begin = w.any.lo & ~(kStepKeys - 1);
+  const int steps = w.any.hi < w.any.lo ? 0 : (w.any.hi + kStepKeys - w.begin) / kStepKeys;
+  w.splits = min(a.splits, max(1, steps / kMinSteps));
+  const int share = (steps + w.splits - 1) / w.splits;
+  w.first = w.split * share;
+  w.last = min(steps, w.first + share);
+  return true;
+}
+
+__device__ __forceinline__ float swap_max16(float v) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, v);
+  const auto h = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+  const uint32_t x = h[0], y = h[1];
+  return fmaxf(__uint_as_float(x), __uint_as_float(y));
+}
+__device__ __forceinline__ float swap_max32(float v) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, v);
+  const auto h = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  const uint32_t x = h[0], y = h[1];
+  return fmaxf(__uint_as_float(x), __uint_as_float(y));
+}
+
+__device__ __forceinline__ uint32_t swap_max_u32(uint32_t v) {  // over lanes 16 and 32 apart
+  const auto x = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  const uint32_t x0 = x[0], x1 = x[1];
+  v = max(x0, x1);
+  const auto y = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  const uint32_t y0 = y[0], y1 = y[1];
+  return max(y0, y1);
+}
+
+__device__ __forceinline__ uint32_t pk_max(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a),
+                                                                __builtin_bit_cast(u16x2, b)));
+}
+// Maxima of the two 16-bit halves over the wave, as a scalar.
+__device__ __forceinline__ uint32_t wave_pk_max(uint32_t v) {
+  v = pk_max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true));
+  v = pk_max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true));
+  v = pk_max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, true));
+  v = pk_max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, true));
+  const auto h = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  const uint32_t h0 = h[0], h1 = h[1];
+  v = pk_max(h0, h1);
+  const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  const uint32_t r0 = r[0], r1 = r[1];
+  return (uint32_t)__builtin_amdgcn_readfirstlane((int)pk_max(r0, r1));
+}
+
+// A scale byte's part in a reference: NaN blocks take none.
+__device__ __forceinline__ uint32_t scale_rank(uint32_t s) { return s == 255 ? 0 : s; }
+// 2^(s - ref + kCodeExponent) as the conversions take it; base = 127 + kCodeExponent - ref.
+__device__ __forceinline__ float block_scale(uint32_t s, int base) {
+  const int e = min(max((int)s + base, 0), 254);
+  return __builtin_bit_cast(float, s == 255 ? 0x7FC00000u : (uint32_t)e << 23);
+}
+
+// The values' reference, which what is summed up carries too: that of the keys
+// taken together, or the one before as long as it is no lower and at most 2^8
+// above, so that it seldom changes.  It may fall as well: a single large value
+// takes no bits from those of other keys.  Not below 64, or what was summed up
+// at 2^59 could leave fp32: values below 2^-55 lose bits.
+constexpr int kFirstValueRef = 127, kLastValueRef = 64;
+__device__ __forceinline__ int value_ref(int before, int top) {
+  const int now = max(top, kLastValueRef);
+  return now > before || now + 8 < before ? now : before;
+}
+
+// Eight codes (two dwords of e4m3, one of e2m1) as a matrix operand.
+template <int FMT> __device__ __forceinline__ half8_t codes_operand(const uint32_t *c, float scale) {
+  half2_t h0, h1, h2, h3;
+  if constexpr (FMT == MX_FP8) {
+    h0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)c[0], scale, 0);
+    h1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)c[0], scale, 1);
+    h2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)c[1], scale, 0);
+    h3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)c[1], scale, 1);
+  } else {
+    h0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c[0], scale, 0);
+    h1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c[0], scale, 1);
+    h2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c[0], scale, 2);
+    h3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c[0], scale, 3);
+  }
+  return half8_t{h0.x, h0.y, h1.x, h1.y, h2.x, h2.y, h3.x, h3.y};
+}
+
+template <int FMT>
+__device__ __forceinline__ bf16x8 codes_operand_bf16(const uint32_t *c, float scale) {
+  bf16x2 h0, h1, h2, h3;
+  if constexpr (FMT == MX_FP8) {
+    h0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)c[0], scale, 0);
+    h1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)c[0], scale, 1);
+    h2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)c[1], scale, 0);
+    h3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)c[1], scale, 1);
+  } else {
+    h0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[0], scale, 0);
+    h1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[0], scale, 1);
+    h2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[0], scale, 2);
+    h3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[0], scale, 3);
+  }
+  return bf16x8{h0.x, h0.y, h1.x, h1.y, h2.x, h2.y, h3.x, h3.y};
+}
+
+// Whether 16 codes or their scale hold a NaN.
+template <int FMT, int W>
+__device__ __forceinline__ bool has_nan(const uint32_t (&c)[W], uint32_t s) {
+  bool r = s == 255;
+  if constexpr (FMT == MX_FP8)
+#pragma unroll
+    for (int i = 0; i < W; i++) r |= (((c[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
+  return r;
+}
+
+// Eight consecutive values of a row of q.
+__device__ __forceinline__ void load_q8(const AttentionArgs &a, int64_t at, float (&f)[8]) {
+  if (a.type == MX_F32)
+    raw8_to_f32<MX_F32>(load_raw8<MX_F32>(static_cast<const float *>(a.q) + at, 0), f);
+  else if (a.type == MX_BF16)
+    raw8_to_f32<MX_BF16>(load_raw8<MX_BF16>(static_cast<const __bf16 *>(a.q) + at, 0), f);
+  else
+    raw8_to_f32<MX_F16>(load_raw8<MX_F16>(static_cast<const _Float16 *>(a.q) + at, 0), f);
+}
+
+__device__ __forceinline__ void store_y4(const AttentionArgs &a, int64_t at, f32x4 v) {
+  if (a.type == MX_F32) {
+    *reinterpret_cast<f32x4 *>(static_cast<float *>(a.y) + at) = v;
+  } else {
+    u32x2 r;
+    if (a.type == MX_BF16) {
+      r[0] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)v[0], (__bf16)v[1]});
+      r[1] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)v[2], (__bf16)v[3]});
+    } else {
+      r[0] = as_u32h(half2_t{(_Float16)v[0], (_Float16)v[1]});
+      r[1] = as_u32h(half2_t{(_Float16)v[2], (_Float16)v[3]});
+    }
+    *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.y) + at) = r;
+  }
+}
+
+// The exponent e of a row whose largest magnitude has these bits (0 for a row of zeros).
+__device__ __forceinline__ int row_exponent(uint32_t amax_bits) {
+  return amax_bits == 0 ? 0 : (int)(amax_bits >> 23) - 127 - 14;
+}
+
+// The share of a partial result whose largest x is m in one whose is most.  A
+// part without keys has m = -inf and zeros; one whose x are all NaN has m =
+// -inf and NaNs, which have to stay.
+__device__ __forceinline__ float part_share(float m, float most) {
+  return m == kMinusInf ? 1.0f : __builtin_amdgcn_exp2f(m - most);
+}
+
+}  // namespace q4k

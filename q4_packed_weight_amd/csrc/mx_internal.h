@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "q4k_mx.h"
+
 namespace q4k {
 
 // Values that the norm and mx_dequantize write, from this many bytes on, an
@@ -60,5 +62,78 @@ struct MoeArgs {
 };
 int64_t moe_workspace_bytes(int64_t T, int64_t H, int64_t F, int64_t E, int64_t k);
 hipError_t mxfp4_moe_launch(const MoeArgs &a, hipStream_t stream);
+
+// Division of 0 <= n < 2^31 by d: n * m >> shift with m = floor(2^shift / d) + 1
+// and shift = 31 + ceil(log2 d), whose excess over n / d stays below 1 / d.
+struct FastDiv {
+  uint32_t m = 0, shift = 0;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t d) {
+    uint32_t l = 0;
+    while (((uint64_t)1 << l) < d) l++;
+    shift = 31 + l;
+    m = (uint32_t)(((uint64_t)1 << shift) / d + 1);
+  }
+  __host__ __device__ uint32_t of(uint32_t n) const { return (uint32_t)((uint64_t)n * m >> shift); }
+};
+
+struct RotaryArgs {
+  const void *x;
+  void *y;
+  const int64_t *positions;
+  const double *frequencies;
+  int64_t x_stride, y_stride;  // values from a token's row to the next
+  float amplitude;
+  int n_tokens, n_heads, head_dim, rotary_dim;
+  int tokens, heads, chunks;  // of a workgroup; chunks of a head
+  FastDiv by_pairs, by_chunks, by_heads;
+};
+hipError_t mx_rotary_launch(const void *x, int64_t x_stride, int type, const int64_t *positions,
+                            const double *frequencies, float amplitude, int64_t n_tokens,
+                            int n_heads, int head_dim, int rotary_dim, bool half, void *y,
+                            int64_t y_stride, hipStream_t stream);
+void mx_rotary_frequencies_make(int d, double base, int scaling, double factor, double trained,
+                                double low, double high, double *f, double *amplitude);
+
+// A paged cache: row (page * heads + head) * page_size + place of each array.
+struct CacheArgs {
+  const void *k, *v;    // of mx_cache_write
+  void *k_out, *v_out;  // of mx_cache_read
+  int64_t k_stride, v_stride;
+  const int64_t *slots;
+  uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+  int64_t n_slots;
+  uint32_t n_chunks;       // of this launch, each of keys and values
+  uint32_t heads, chunks;  // chunks of eight values of a head
+  uint32_t page_size;
+  FastDiv by_chunks, by_heads, by_page;
+};
+__device__ __forceinline__ int64_t cache_row(const CacheArgs &a, int64_t slot, uint32_t head) {
+  const uint32_t page = a.by_page.of((uint32_t)slot), place = (uint32_t)slot - page * a.page_size;
+  return ((int64_t)page * a.heads + head) * a.page_size + place;
+}
+hipError_t mx_cache_write_launch(const CacheArgs &a, int64_t n_tokens, int type, int format,
+                                 hipStream_t stream);
+hipError_t mx_cache_read_launch(const CacheArgs &a, int64_t n_tokens, int type, int format,
+                                hipStream_t stream);
+
+struct AttentionArgs {
+  const void *q;
+  void *y;
+  int64_t q_stride, y_stride;
+  const int32_t *starts, *counts, *table;
+  const uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+  float *partial;  // [rows][splits][head_dim], then [rows][splits][2]
+  int64_t n_rows;  // n_tokens * n_heads
+  int type, format, n_tokens, n_heads, n_kv_heads, group, head_dim;
+  int n_seqs, pages_per_seq, max_queries, n_pages, page_size;
+  int causal, window;  // window 0: none
+  int splits, tiles;   // ranges of keys; tiles of rows
+  float scale;         // times log2(e)
+  FastDiv by_page, by_group, by_kv_heads, by_tiles, by_splits;
+};
+// Sizes alone decide the launch: the same call has the same workspace.
+int64_t mx_attention_workspace_bytes(AttentionArgs &a);
+hipError_t mx_attention_launch(const AttentionArgs &a, hipStream_t stream);
 
 }  // namespace q4k

@@ -4,6 +4,7 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <cmath>
 #include <mutex>
 #include <vector>
 
@@ -182,6 +183,60 @@ bool valid_moe_dims(int64_t T, int64_t H, int64_t F, int64_t E, int64_t k) {
   return T > 0 && T <= kMaxMxTokens && H > 0 && H % 32 == 0 && H <= kMaxMoeDim && F > 0 &&
          F % 32 == 0 && F <= kMaxMoeDim && E > 0 && E <= q4k::kMoeMaxExperts && k > 0 && k <= E &&
          k <= q4k::kMoeMaxTopK;
+}
+
+// The sizes of the attention operators.
+constexpr int64_t kMaxHeads = 4096;
+constexpr int64_t kMaxRotaryDim = 512;
+bool valid_count(int64_t n) { return n > 0 && n <= 0x7FFFFFFF; }
+bool valid_heads(int64_t n) { return n > 0 && n <= kMaxHeads; }
+bool valid_cache(int64_t n_tokens, int64_t n_heads, int64_t head_dim, int64_t n_pages,
+                 int64_t page_size) {
+  return valid_count(n_tokens) && valid_heads(n_heads) && head_dim > 0 && head_dim % 32 == 0 &&
+         head_dim <= 256 && page_size > 0 && page_size <= 65536 && valid_count(n_pages) &&
+         n_pages * page_size <= 0x7FFFFFFF;
+}
+// Rows of `width` values with this many to the next, at most 2^31 of them.
+bool valid_stride(int64_t stride, int64_t width) { return stride >= width && stride <= 0x7FFFFFFF; }
+bool aligned_rows(const void *p, int64_t stride, int type) {
+  return aligned16(p) && stride * (type == MX_F32 ? 4 : 2) % 16 == 0;
+}
+
+q4k::CacheArgs cache_args(const int64_t *slots, int64_t n_heads, int64_t head_dim, int64_t n_pages,
+                          int64_t page_size) {
+  q4k::CacheArgs a = {};
+  a.slots = slots;
+  a.n_slots = n_pages * page_size;
+  a.heads = (uint32_t)n_heads;
+  a.chunks = (uint32_t)(head_dim / 8);
+  a.page_size = (uint32_t)page_size;
+  a.by_chunks = q4k::FastDiv(a.chunks);
+  a.by_heads = q4k::FastDiv(a.heads);
+  a.by_page = q4k::FastDiv(a.page_size);
+  return a;
+}
+
+bool attention_args(q4k::AttentionArgs &a, int64_t n_tokens, int64_t n_heads, int64_t n_kv_heads,
+                    int64_t head_dim, int64_t n_seqs, int64_t pages_per_seq, int64_t page_size,
+                    int64_t max_queries) {
+  constexpr int64_t kMostKeys = ((int64_t)1 << 30) - 1, kMostTiles = ((int64_t)1 << 24) - 1;
+  if (!valid_cache(n_tokens, n_kv_heads, head_dim, 1, page_size) || !valid_heads(n_heads) ||
+      n_heads % n_kv_heads != 0 || !valid_count(n_seqs) || !valid_count(pages_per_seq) ||
+      !valid_count(max_queries) || pages_per_seq * page_size > kMostKeys ||
+      n_seqs > kMostTiles || max_queries * (n_heads / n_kv_heads) > 0x7FFFFFFF - 16 ||
+      (max_queries * (n_heads / n_kv_heads) + 15) / 16 * n_kv_heads > kMostTiles / n_seqs)
+    return false;
+  a.n_tokens = (int)n_tokens;
+  a.n_heads = (int)n_heads;
+  a.n_kv_heads = (int)n_kv_heads;
+  a.group = (int)(n_heads / n_kv_heads);
+  a.n_rows = n_tokens * n_heads;
+  a.head_dim = (int)head_dim;
+  a.n_seqs = (int)n_seqs;
+  a.pages_per_seq = (int)pages_per_seq;
+  a.page_size = (int)page_size;
+  a.max_queries = (int)max_queries;
+  return true;
 }
 
 }  // namespace
@@ -653,6 +708,159 @@ int mxfp4_moe(const void *x, int type, const void *router, const float *router_b
   return Q4K_OK;
 }
 
+int mx_rotary(const void *x, int64_t x_stride, int type, const int64_t *positions,
+              const double *frequencies, float amplitude, int64_t n_tokens, int64_t n_heads,
+              int64_t head_dim, int64_t rotary_dim, int layout, void *y, int64_t y_stride,
+              void *stream) {
+  if (!valid_count(n_tokens) || !valid_heads(n_heads) || head_dim <= 0 || head_dim % 8 != 0 ||
+      head_dim > kMaxRotaryDim || rotary_dim < 2 || rotary_dim % 2 != 0 || rotary_dim > head_dim ||
+      !valid_stride(x_stride, n_heads * head_dim) || !valid_stride(y_stride, n_heads * head_dim))
+    return Q4K_EINVAL_DIM;
+  if (!valid_mx_type(type) || (layout != MX_ROTARY_HALF && layout != MX_ROTARY_INTERLEAVED))
+    return Q4K_EINVAL_TYPE;
+  if (!x || !positions || !frequencies || !y) return Q4K_ENULL;
+  if (!aligned_rows(x, x_stride, type) || !aligned_rows(y, y_stride, type) ||
+      (((uintptr_t)positions | (uintptr_t)frequencies) & 7u) != 0)
+    return Q4K_EALIGN;
+  hipError_t e = q4k::mx_rotary_launch(x, x_stride, type, positions, frequencies, amplitude,
+                                       n_tokens, (int)n_heads, (int)head_dim, (int)rotary_dim,
+                                       layout == MX_ROTARY_HALF, y, y_stride, (hipStream_t)stream);
+  return e == hipSuccess ? Q4K_OK : hip_fail(e, "mx_rotary launch");
+}
+
+int mx_rotary_frequencies(int64_t rotary_dim, double base, int scaling, double factor,
+                          double trained, double low, double high, double *frequencies,
+                          double *amplitude) {
+  if (rotary_dim < 2 || rotary_dim % 2 != 0 || rotary_dim > kMaxRotaryDim) return Q4K_EINVAL_DIM;
+  if (scaling < MX_ROTARY_NONE || scaling > MX_ROTARY_BANDS) return Q4K_EINVAL_TYPE;
+  const bool between = scaling == MX_ROTARY_YARN || scaling == MX_ROTARY_BANDS;
+  if (!(base > 1.0) || !std::isfinite(base) ||
+      (scaling != MX_ROTARY_NONE && (!(factor >= 1.0) || !std::isfinite(factor))) ||
+      (between && (!(trained >= 1.0) || !std::isfinite(trained) || !(low > 0.0) ||
+                   !(high > low) || !std::isfinite(high))))
+    return Q4K_EINVAL_DIM;
+  if (!frequencies || !amplitude) return Q4K_ENULL;
+  q4k::mx_rotary_frequencies_make((int)rotary_dim, base, scaling, factor, trained, low, high,
+                                  frequencies, amplitude);
+  return Q4K_OK;
+}
+
+int mx_cache_write(const void *k, int64_t k_stride, const void *v, int64_t v_stride, int type,
+                   const int64_t *slots, int64_t n_tokens, int64_t n_heads, int64_t head_dim,
+                   int format, uint8_t *k_codes, uint8_t *k_scales, uint8_t *v_codes,
+                   uint8_t *v_scales, int64_t n_pages, int64_t page_size, void *stream) {
+  if (!valid_cache(n_tokens, n_heads, head_dim, n_pages, page_size) ||
+      !valid_stride(k_stride, n_heads * head_dim) || !valid_stride(v_stride, n_heads * head_dim))
+    return Q4K_EINVAL_DIM;
+  if (!valid_mx_type(type) || !valid_mx_format(format)) return Q4K_EINVAL_TYPE;
+  if (!k || !v || !slots || !k_codes || !k_scales || !v_codes || !v_scales) return Q4K_ENULL;
+  if (!aligned_rows(k, k_stride, type) || !aligned_rows(v, v_stride, type) ||
+      !aligned16(k_codes) || !aligned16(v_codes) || ((uintptr_t)slots & 7u) != 0)
+    return Q4K_EALIGN;
+  q4k::CacheArgs a = cache_args(slots, n_heads, head_dim, n_pages, page_size);
+  a.k = k;
+  a.v = v;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.k_codes = k_codes;
+  a.k_scales = k_scales;
+  a.v_codes = v_codes;
+  a.v_scales = v_scales;
+  hipError_t e = q4k::mx_cache_write_launch(a, n_tokens, type, format, (hipStream_t)stream);
+  return e == hipSuccess ? Q4K_OK : hip_fail(e, "mx_cache_write launch");
+}
+
+int mx_cache_read(const int64_t *slots, int64_t n_tokens, int64_t n_heads, int64_t head_dim,
+                  int format, const uint8_t *k_codes, const uint8_t *k_scales,
+                  const uint8_t *v_codes, const uint8_t *v_scales, int64_t n_pages,
+                  int64_t page_size, void *k, int64_t k_stride, void *v, int64_t v_stride,
+                  int type, void *stream) {
+  if (!valid_cache(n_tokens, n_heads, head_dim, n_pages, page_size) ||
+      !valid_stride(k_stride, n_heads * head_dim) || !valid_stride(v_stride, n_heads * head_dim))
+    return Q4K_EINVAL_DIM;
+  if (!valid_mx_type(type) || !valid_mx_format(format)) return Q4K_EINVAL_TYPE;
+  if (!k || !v || !slots || !k_codes || !k_scales || !v_codes || !v_scales) return Q4K_ENULL;
+  if (!aligned_rows(k, k_stride, type) || !aligned_rows(v, v_stride, type) ||
+      !aligned16(k_codes) || !aligned16(v_codes) || ((uintptr_t)slots & 7u) != 0)
+    return Q4K_EALIGN;
+  q4k::CacheArgs a = cache_args(slots, n_heads, head_dim, n_pages, page_size);
+  a.k_out = k;
+  a.v_out = v;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.k_codes = const_cast<uint8_t *>(k_codes);
+  a.k_scales = const_cast<uint8_t *>(k_scales);
+  a.v_codes = const_cast<uint8_t *>(v_codes);
+  a.v_scales = const_cast<uint8_t *>(v_scales);
+  hipError_t e = q4k::mx_cache_read_launch(a, n_tokens, type, format, (hipStream_t)stream);
+  return e == hipSuccess ? Q4K_OK : hip_fail(e, "mx_cache_read launch");
+}
+
+int64_t mx_attention_workspace_size(int64_t n_tokens, int64_t n_heads, int64_t n_kv_heads,
+                                    int64_t head_dim, int64_t n_seqs, int64_t pages_per_seq,
+                                    int64_t page_size, int64_t max_queries) {
+  q4k::AttentionArgs a = {};
+  if (!attention_args(a, n_tokens, n_heads, n_kv_heads, head_dim, n_seqs, pages_per_seq, page_size,
+                      max_queries))
+    return Q4K_EINVAL_DIM;
+  return q4k::mx_attention_workspace_bytes(a);
+}
+
+int mx_attention(const void *q, int64_t q_stride, int type, const int32_t *query_starts,
+                 const int32_t *key_counts, const int32_t *pages, int64_t n_tokens,
+                 int64_t n_heads, int64_t n_kv_heads, int64_t head_dim, int64_t n_seqs,
+                 int64_t pages_per_seq, int64_t max_queries, float scale, int causal,
+                 int64_t window, int format, const uint8_t *k_codes, const uint8_t *k_scales,
+                 const uint8_t *v_codes, const uint8_t *v_scales, int64_t n_pages,
+                 int64_t page_size, void *y, int64_t y_stride, void *workspace,
+                 int64_t workspace_bytes, void *stream) {
+  q4k::AttentionArgs a = {};
+  if (!attention_args(a, n_tokens, n_heads, n_kv_heads, head_dim, n_seqs, pages_per_seq, page_size,
+                      max_queries) ||
+      !valid_cache(n_tokens, n_kv_heads, head_dim, n_pages, page_size) ||
+      !valid_stride(q_stride, n_heads * head_dim) || !valid_stride(y_stride, n_heads * head_dim) ||
+      !std::isfinite(scale) || window < 0 || (window > 0 && !causal))
+    return Q4K_EINVAL_DIM;
+  if (!valid_mx_type(type) || !valid_mx_format(format)) return Q4K_EINVAL_TYPE;
+  const int64_t need = q4k::mx_attention_workspace_bytes(a);
+  if (!q || !query_starts || !key_counts || !pages || !k_codes || !k_scales || !v_codes ||
+      !v_scales || !y || (need > 0 && !workspace))
+    return Q4K_ENULL;
+  if (!aligned_rows(q, q_stride, type) || !aligned_rows(y, y_stride, type) ||
+      !aligned16(k_codes) || !aligned16(v_codes) || ((uintptr_t)workspace & 255u) != 0 ||
+      (((uintptr_t)query_starts | (uintptr_t)key_counts | (uintptr_t)pages) & 3u) != 0)
+    return Q4K_EALIGN;
+  if (workspace_bytes < need) {
+    snprintf(g_hip_detail, sizeof g_hip_detail,
+             "mx_attention: the scratch workspace is smaller than mx_attention_workspace_size");
+    return Q4K_ESCRATCH;
+  }
+  a.q = q;
+  a.y = y;
+  a.q_stride = q_stride;
+  a.y_stride = y_stride;
+  a.starts = query_starts;
+  a.counts = key_counts;
+  a.table = pages;
+  a.k_codes = k_codes;
+  a.k_scales = k_scales;
+  a.v_codes = v_codes;
+  a.v_scales = v_scales;
+  a.partial = static_cast<float *>(workspace);
+  a.type = type;
+  a.format = format;
+  a.n_pages = (int)n_pages;
+  a.causal = causal != 0;
+  // no sequence has more keys than 2^30: a longer window is none
+  a.window = window > ((int64_t)1 << 30) ? 0 : (int)window;
+  a.scale = scale * 1.44269504088896340736f;
+  a.by_page = q4k::FastDiv((uint32_t)page_size);
+  a.by_group = q4k::FastDiv((uint32_t)a.group);
+  a.by_kv_heads = q4k::FastDiv((uint32_t)a.n_kv_heads);
+  hipError_t e = q4k::mx_attention_launch(a, (hipStream_t)stream);
+  return e == hipSuccess ? Q4K_OK : hip_fail(e, "mx_attention launch");
+}
+
 const char *q4k_strerror(int code) {
   switch (code) {
     case Q4K_OK: return "ok";
@@ -664,7 +872,7 @@ const char *q4k_strerror(int code) {
     case Q4K_EALIGN:
       return "x and the Q4_K, Q4_0 or Q6_K blocks must be 16-byte aligned (MX: values and codes "
              "too, the workspace 256-byte aligned)";
-    case Q4K_EINVAL_TYPE: return "unknown value type or MX format";
+    case Q4K_EINVAL_TYPE: return "unknown value type, MX format or rotary layout or scaling";
     case Q4K_EHIP: return g_hip_detail[0] ? g_hip_detail : "HIP runtime error";
     case Q4K_ESCRATCH:
       return g_hip_detail[0] ? g_hip_detail
