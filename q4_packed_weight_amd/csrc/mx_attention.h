@@ -60,11 +60,10 @@ __device__ __forceinline__ Sequence sequence_of(const AttentionArgs &a, int s) {
   return r;
 }
 
-// 32 keys make a step; each range of keys has at least kMinSteps of them.
-constexpr int kStepKeys = 32;
-constexpr int kMinSteps = 8;
+// Each range of keys has at least so many.
+constexpr int kMinKeys = 256;
 
-// What one workgroup works on: rows r0 .. of a sequence's (token, head of the
+// What one workgroup works on, in steps of KEYS keys: rows r0 .. of a sequence's (token, head of the
 // group) pairs and the steps of keys that any of them sees, or its share.
 struct Work {
   Sequence seq;
@@ -73,7 +72,7 @@ struct Work {
   int begin, first, last;  // key of step 0; this share's steps
 };
 
-template <int ROWS>
+template <int ROWS, int KEYS>
 __device__ __forceinline__ bool work_of(const AttentionArgs &a, uint32_t block, int splits, Work &w) {
   uint32_t n = a.by_kv_heads.of(block);
   w.kv_head = block - n * a.n_kv_heads;
@@ -81,7 +80,7 @@ __device__ __forceinline__ bool work_of(const AttentionArgs &a, uint32_t block, 
   w.split = n - n2 * splits;
   const uint32_t s = a.by_tiles.of(n2);
   w.index = s;
-  w.r0 = (n2 - s * a.tiles) * ROWS;
+  w.r0 = (a.tiles - 1 - (n2 - s * a.tiles)) * ROWS;  // those with most keys first
   w.seq = sequence_of(a, s);
   const int all_rows = w.seq.nq * a.group;
   if (w.r0 >= all_rows) return false;
@@ -90,9 +89,9 @@ __device__ __forceinline__ bool work_of(const AttentionArgs &a, uint32_t block, 
   const Range two = w.seq.sees(a, a.by_group.of(w.r0 + w.rows - 1));
   w.any = {one.lo, two.hi};
   w.all = {two.lo, one.hi};
-  w.begin = w.any.lo & ~(kStepKeys - 1);
-  const int steps = w.any.hi < w.any.lo ? 0 : (w.any.hi + kStepKeys - w.begin) / kStepKeys;
-  w.splits = min(a.splits, max(1, steps / kMinSteps));
+  w.begin = w.any.lo & ~(KEYS - 1);
+  const int steps = w.any.hi < w.any.lo ? 0 : (w.any.hi + KEYS - w.begin) / KEYS;
+  w.splits = min(a.splits, max(1, steps / (kMinKeys / KEYS)));
   const int share = (steps + w.splits - 1) / w.splits;
   w.first = w.split * share;
   w.last = min(steps, w.first + share);
@@ -175,6 +174,16 @@ template <int FMT> __device__ __forceinline__ half8_t codes_operand(const uint32
   return half8_t{h0.x, h0.y, h1.x, h1.y, h2.x, h2.y, h3.x, h3.y};
 }
 
+template <int W> __device__ __forceinline__ void load_codes(const uint8_t *p, uint32_t (&c)[W]) {
+  if constexpr (W == 4) {
+    const u32x4 v = *reinterpret_cast<const u32x4 *>(p);
+    c[0] = v[0]; c[1] = v[1]; c[2] = v[2]; c[3] = v[3];
+  } else {
+    const u32x2 v = *reinterpret_cast<const u32x2 *>(p);
+    c[0] = v[0]; c[1] = v[1];
+  }
+}
+
 template <int FMT>
 __device__ __forceinline__ bf16x8 codes_operand_bf16(const uint32_t *c, float scale) {
   bf16x2 h0, h1, h2, h3;
@@ -239,5 +248,9 @@ __device__ __forceinline__ int row_exponent(uint32_t amax_bits) {
 __device__ __forceinline__ float part_share(float m, float most) {
   return m == kMinusInf ? 1.0f : __builtin_amdgcn_exp2f(m - most);
 }
+
+// 128 rows a workgroup, 64 keys a step.
+constexpr int kTiledRows = 128, kTiledKeys = 64;
+hipError_t attention_tiled_launch(const AttentionArgs &a, int blocks, hipStream_t stream);
 
 }  // namespace q4k

@@ -7,6 +7,7 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kRows = 16;
+constexpr int kStepKeys = 32;
 
 // One wave's 32 keys (lane: key l % 16 of two tiles, group g = l / 16 of its
 // dims: 64 p + 16 g .. + 15 for p < ND) as they lie in memory.
@@ -16,16 +17,6 @@ template <int FMT, int ND> struct StepData {
   uint32_t ks[2][ND], vs[2][ND];
   uint32_t ok;  // bit by key, the same in every lane
 };
-
-template <int W> __device__ __forceinline__ void load_codes(const uint8_t *p, uint32_t (&c)[W]) {
-  if constexpr (W == 4) {
-    const u32x4 v = *reinterpret_cast<const u32x4 *>(p);
-    c[0] = v[0]; c[1] = v[1]; c[2] = v[2]; c[3] = v[3];
-  } else {
-    const u32x2 v = *reinterpret_cast<const u32x2 *>(p);
-    c[0] = v[0]; c[1] = v[1];
-  }
-}
 
 // Scores are products S^T = K Q^T of 16 keys by 16 rows: a lane's result is of
 // its row l % 16 and keys 4g .. 4g+3, so that a row's statistics are a lane's
@@ -44,7 +35,7 @@ __global__ __launch_bounds__(kWaves * 64) void attention_rows_kernel(AttentionAr
   __shared__ float2 stats[kWaves][kRows];
   __shared__ __attribute__((aligned(16))) float powers[kWaves][kStepKeys];
   Work w;
-  if (!work_of<kRows>(a, blockIdx.x, a.splits, w) || w.split >= w.splits) return;
+  if (!work_of<kRows, kStepKeys>(a, blockIdx.x, a.splits, w) || w.split >= w.splits) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
   const int D = a.head_dim, nb = D / 32;
   const int64_t code_row = FMT == MX_FP8 ? D : D / 2;
@@ -374,10 +365,11 @@ __global__ __launch_bounds__(kWaves * 64) void attention_rows_kernel(AttentionAr
 }
 
 // The ranges' results joined, a row to 16 lanes.
+template <int ROWS, int KEYS>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a) {
   Work w;
-  if (!work_of<kRows>(a, blockIdx.x, 1, w) || w.splits == 1) return;
-  const int out = threadIdx.x >> 4, D = a.head_dim;
+  if (!work_of<ROWS, KEYS>(a, blockIdx.x, 1, w) || w.splits == 1) return;
+  const int out = 16 * blockIdx.y + (threadIdx.x >> 4), D = a.head_dim;
   if (out >= w.rows) return;
   const int row = w.r0 + out, token = a.by_group.of(row);
   const int head = w.kv_head * a.group + row - token * a.group;
@@ -397,15 +389,19 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a) {
   }
 }
 
+// More than one tile of 16 rows: the form for many rows.
+bool tiled(const AttentionArgs &a) { return (int64_t)a.max_queries * a.group > kRows; }
+
 }  // namespace
 
 // Ranges of keys so that about four workgroups come to a CU, none for fewer
-// than kMinSteps steps.
+// than kMinKeys keys.
 int64_t mx_attention_workspace_bytes(AttentionArgs &a) {
-  a.tiles = (int)(((int64_t)a.max_queries * a.group + kRows - 1) / kRows);
+  const int rows = tiled(a) ? kTiledRows : kRows;
+  a.tiles = (int)(((int64_t)a.max_queries * a.group + rows - 1) / rows);
   const int64_t blocks = (int64_t)a.n_seqs * a.tiles * a.n_kv_heads;
-  const int64_t most = ((int64_t)a.pages_per_seq * a.page_size + kStepKeys - 1) / kStepKeys / kMinSteps;
-  const int64_t want = 1024 / blocks;
+  const int64_t most = (int64_t)a.pages_per_seq * a.page_size / kMinKeys;
+  const int64_t want = (tiled(a) ? 512 : 1024) / blocks;
   a.splits = (int)(want < most ? (want > 1 ? want : 1) : (most > 1 ? most : 1));
   a.by_tiles = FastDiv(a.tiles);
   a.by_splits = FastDiv(a.splits);
@@ -414,8 +410,12 @@ int64_t mx_attention_workspace_bytes(AttentionArgs &a) {
 
 hipError_t mx_attention_launch(const AttentionArgs &a, hipStream_t stream) {
   const int blocks = a.n_seqs * a.tiles * a.n_kv_heads;
-  const int nd = (a.head_dim + 63) / 64;
-#define GO(NP, F, ND)                                                                       \
+  hipError_t e;
+  if (tiled(a)) {
+    e = attention_tiled_launch(a, blocks * a.splits, stream);
+  } else {
+    const int nd = (a.head_dim + 63) / 64;
+#define GO(NP, F, ND)                                                                         \
   hipLaunchKernelGGL((attention_rows_kernel<NP, F, ND>), dim3(blocks * a.splits), dim3(256), 0, \
                      stream, a)
 #define BY_DIM(NP, F)                    \
@@ -425,16 +425,22 @@ hipError_t mx_attention_launch(const AttentionArgs &a, hipStream_t stream) {
     case 3: GO(NP, F, 3); break;         \
     default: GO(NP, F, 4); break;        \
   }
-  if (a.type == MX_F32) {
-    if (a.format == MX_FP4) { BY_DIM(2, MX_FP4) } else { BY_DIM(2, MX_FP8) }
-  } else {
-    if (a.format == MX_FP4) { BY_DIM(1, MX_FP4) } else { BY_DIM(1, MX_FP8) }
-  }
+    if (a.type == MX_F32) {
+      if (a.format == MX_FP4) { BY_DIM(2, MX_FP4) } else { BY_DIM(2, MX_FP8) }
+    } else {
+      if (a.format == MX_FP4) { BY_DIM(1, MX_FP4) } else { BY_DIM(1, MX_FP8) }
+    }
 #undef BY_DIM
 #undef GO
-  hipError_t e = hipGetLastError();
+    e = hipGetLastError();
+  }
   if (e != hipSuccess || a.splits == 1) return e;
-  hipLaunchKernelGGL(attention_join_kernel, dim3(blocks), dim3(256), 0, stream, a);
+  if (tiled(a))
+    hipLaunchKernelGGL((attention_join_kernel<kTiledRows, kTiledKeys>), dim3(blocks, kTiledRows / 16),
+                       dim3(256), 0, stream, a);
+  else
+    hipLaunchKernelGGL((attention_join_kernel<kRows, kStepKeys>), dim3(blocks), dim3(256), 0, stream,
+                       a);
   return hipGetLastError();
 }
 

@@ -1,0 +1,452 @@
+// mx_attention_tiled.hip -- attention over a paged MX cache for many rows:
+// chunks of new tokens, 32 rows a wave.
+#include "mx_attention.h"
+
+namespace q4k {
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kRows = kTiledRows;
+constexpr int kTile = kTiledKeys;
+static_assert(kRows == 32 * kWaves, "32 rows a wave");
+constexpr int kWaveKeys = kTile / kWaves;  // that a wave stages: 16, one step of V^T P^T
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// What a wave says of the 16 keys it has staged.
+struct Staged {
+  uint32_t word;
+  __device__ __forceinline__ int k_ref() const { return word & 255; }
+  __device__ __forceinline__ int v_ref() const { return word >> 8 & 255; }
+  __device__ __forceinline__ bool missing() const { return word >> 16 & 1; }
+  __device__ __forceinline__ bool nans() const { return word >> 17 & 1; }
+};
+
+// A wave's share of a tile as it lies in memory: 16 codes (dims 16 n .. of lane
+// n of a key's LP lanes) in each pass.
+template <int FMT, int ND> struct TileData {
+  static constexpr int LP = ND == 1 ? 4 : ND == 2 ? 8 : 16;
+  static constexpr int PASSES = kWaveKeys * LP / 64;
+  static constexpr int W = FMT == MX_FP8 ? 4 : 2;
+  uint32_t k[PASSES][W], v[PASSES][W], ks[PASSES], vs[PASSES];
+  bool ok[PASSES];
+};
+
+template <int LP> __device__ __forceinline__ uint32_t max_of_key(uint32_t v) {
+  v = max_dpp_step<0xB1>(v);
+  v = max_dpp_step<0x4E>(v);
+  if constexpr (LP >= 8) v = max_dpp_step<0x141>(v);
+  if constexpr (LP >= 16) v = max_dpp_step<0x140>(v);
+  return v;
+}
+
+template <int NP, int FMT, int ND>
+__global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_kernel(AttentionArgs a) {
+  constexpr int DP = 64 * ND;
+  constexpr int KS = 2 * DP + 16, VS = 2 * DP + 32;  // bytes of a key's row in LDS
+  constexpr int X = kCodeExponent<FMT>;
+  typedef TileData<FMT, ND> Data;
+  constexpr int LP = Data::LP, PASSES = Data::PASSES, W = Data::W;
+  __shared__ __attribute__((aligned(16))) uint8_t k_lds[2][kTile * KS];
+  __shared__ __attribute__((aligned(16))) uint8_t v_lds[2][kTile * VS];
+  __shared__ __attribute__((aligned(16))) float powers[2][kTile];
+  __shared__ __attribute__((aligned(16))) uint32_t staged[2][kWaves];
+  Work w;
+  if (!work_of<kRows, kTile>(a, blockIdx.x, a.splits, w) || w.split >= w.splits) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r32 = lane & 31, half = lane >> 5;
+  const int D = a.head_dim, nb = D / 32;
+  const int64_t code_row = FMT == MX_FP8 ? D : D / 2;
+
+  // queries: dims 16 s + 8 half .. + 7 in step s; rows behind the last are its copies
+  const bool active = 32 * wave < w.rows;
+  const int last_row = w.r0 + w.rows - 1;
+  const int row = min(w.r0 + 32 * wave + r32, last_row);
+  const int token = a.by_group.of(row);
+  const Range mine = w.seq.sees(a, token);
+  const Range one = w.seq.sees(a, a.by_group.of(min(w.r0 + 32 * wave, last_row)));
+  const Range two = w.seq.sees(a, a.by_group.of(min(w.r0 + 32 * wave + 31, last_row)));
+  half8_t q[NP][DP / 16];
+  float row_scale;
+  {
+    const int64_t at = (int64_t)(w.seq.q0 + token) * a.q_stride +
+                       (int64_t)(w.kv_head * a.group + row - token * a.group) * D + 8 * half;
+    float f[DP / 16][8];
+    uint32_t amax = 0;
+#pragma unroll
+    for (int s = 0; s < DP / 16; s++) {
+      if (16 * s < D) load_q8(a, at + 16 * s, f[s]);
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        if (16 * s >= D) f[s][i] = 0.0f;
+        const uint32_t b = __builtin_bit_cast(uint32_t, f[s][i]) & 0x7FFFFFFFu;
+        amax = b > amax ? b : amax;
+      }
+    }
+    const auto y = __builtin_amdgcn_permlane32_swap(amax, amax, false, false);
+    const uint32_t y0 = y[0], y1 = y[1];
+    amax = max(y0, y1);
+    const int e = row_exponent(amax);
+    // the largest x is the largest score: a negative scale's sign goes to q
+    const float sign = a.scale < 0.0f ? -1.0f : 1.0f;
+    row_scale = amax >= 0x7F800000u ? __builtin_nanf("") : __builtin_ldexpf(a.scale * sign, e);
+#pragma unroll
+    for (int s = 0; s < DP / 16; s++)
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        const float v = __builtin_ldexpf(f[s][i] * sign, -e);
+        q[0][s][i] = (_Float16)v;
+        if constexpr (NP == 2) q[1][s][i] = (_Float16)(v - (float)q[0][s][i]);
+      }
+  }
+
+  const int32_t *const table = a.table + (int64_t)w.index * a.pages_per_seq;
+  const int sub = lane & (LP - 1), lane_key = lane / LP;
+  const bool has = 16 * sub < D;
+  const auto load = [&](int t, Data &d) {
+#pragma unroll
+    for (int p = 0; p < PASSES; p++) {
+      const int key = w.begin + t * kTile + kWaveKeys * wave + 64 / LP * p + lane_key;
+      bool ok = t < w.last && key >= w.any.lo && key <= w.any.hi;
+      int page = 0, at = 0;
+      if (ok) {
+        at = a.by_page.of(key);
+        page = table[at];
+        ok = page >= 0 && page < a.n_pages;
+      }
+      const int64_t r = ((int64_t)page * a.n_kv_heads + w.kv_head) * a.page_size +
+                        (key - at * a.page_size);
+      d.ok[p] = ok;
+      d.ks[p] = d.vs[p] = 0;
+#pragma unroll
+      for (int i = 0; i < W; i++) d.k[p][i] = d.v[p][i] = 0;
+      if (ok && has) {
+        const int64_t c = r * code_row + 16 * sub * (FMT == MX_FP8 ? 2 : 1) / 2;
+        const int64_t s = r * nb + (sub >> 1);
+        load_codes(a.k_codes + c, d.k[p]);
+        load_codes(a.v_codes + c, d.v[p]);
+        d.ks[p] = a.k_scales[s];
+        d.vs[p] = a.v_scales[s];
+      }
+    }
+  };
+  const auto is_mixed = [&](int t) {
+    const int first = w.begin + t * kTile;
+    return max(first, w.any.lo) < w.all.lo || min(first + kTile - 1, w.any.hi) > w.all.hi;
+  };
+
+  // The tile's share into LDS as fp16 (bf16 values where it is mixed).
+  const auto stage = [&](int t, const Data &d, int k_before, int v_before) {
+    const int b = t & 1;
+    const bool mixed = is_mixed(t);
+    uint32_t top = 0;
+    bool missing = false, nan = false;
+#pragma unroll
+    for (int p = 0; p < PASSES; p++) {
+      top = pk_max(top, scale_rank(d.ks[p]) | scale_rank(d.vs[p]) << 16);
+      missing |= !d.ok[p];
+    }
+    top = wave_pk_max(top);
+    missing = __builtin_amdgcn_ballot_w64(missing) != 0;
+    const int k_ref = value_ref(k_before, top & 0xFFFF), v_ref = value_ref(v_before, top >> 16);
+#pragma unroll
+    for (int p = 0; p < PASSES; p++) {
+      const int n = kWaveKeys * wave + 64 / LP * p + lane_key;
+      uint8_t *const k_to = k_lds[b] + n * KS + 32 * sub, *const v_to = v_lds[b] + n * VS + 32 * sub;
+      int k_base = 127 + X - k_ref;
+      if (mixed) {
+        const int own = (int)max_of_key<LP>(scale_rank(d.ks[p]));
+        k_base = 127 + X - own;
+        nan |= has_nan<FMT>(d.v[p], d.vs[p]);
+        if (sub == 0) powers[b][n] = d.ok[p] ? __builtin_ldexpf(1.0f, own - X - 127) : -1.0f;
+        if (LP * 16 == DP || 16 * sub < DP) {
+          const float s = block_scale(d.vs[p], 0);
+          *reinterpret_cast<bf16x8 *>(v_to) = codes_operand_bf16<FMT>(&d.v[p][0], s);
+          *reinterpret_cast<bf16x8 *>(v_to + 16) = codes_operand_bf16<FMT>(&d.v[p][W / 2], s);
+        }
+      } else {
+        if (missing && sub == 0) powers[b][n] = d.ok[p] ? 1.0f : -1.0f;
+        if (LP * 16 == DP || 16 * sub < DP) {
+          const float s = block_scale(d.vs[p], 127 + X - v_ref);
+          *reinterpret_cast<half8_t *>(v_to) = codes_operand<FMT>(&d.v[p][0], s);
+          *reinterpret_cast<half8_t *>(v_to + 16) = codes_operand<FMT>(&d.v[p][W / 2], s);
+        }
+      }
+      if (LP * 16 == DP || 16 * sub < DP) {
+        const float s = block_scale(d.ks[p], k_base);
+        *reinterpret_cast<half8_t *>(k_to) = codes_operand<FMT>(&d.k[p][0], s);
+        *reinterpret_cast<half8_t *>(k_to + 16) = codes_operand<FMT>(&d.k[p][W / 2], s);
+      }
+    }
+    if (mixed) nan = __builtin_amdgcn_ballot_w64(nan) != 0;
+    if (lane == 0)
+      staged[b][wave] = (uint32_t)k_ref | (uint32_t)v_ref << 8 | (missing ? 1u << 16 : 0) |
+                        (nan ? 1u << 17 : 0);
+  };
+
+  f32x16 acc[2 * ND];
+#pragma unroll
+  for (int t = 0; t < 2 * ND; t++)
+#pragma unroll
+    for (int i = 0; i < 16; i++) acc[t][i] = 0.0f;
+  float m = kMinusInf, l = 0.0f;
+  int k_ref = kFirstValueRef, v_ref = kFirstValueRef;
+  typedef __attribute__((address_space(3))) s16x4 LdsS16x4;
+  const int v_at = (4 * half + (lane >> 2 & 3)) * VS + 32 * (lane >> 4 & 1) + 8 * (lane & 3);
+  const int k_at = r32 * KS + 16 * half;
+
+  // 32 dims of the 16 keys of step n, transposed: keys 4 half .. + 3 and 8 + 4 half .. + 3
+  const auto value_operand = [&](int b, int n, int t) {
+    const uint8_t *const at = v_lds[b] + v_at + 16 * n * VS + 64 * t;
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsS16x4 *)at);
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsS16x4 *)(at + 8 * VS));
+    return s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  };
+  const auto scores = [&](int b, f32x16 (&s)[2]) {
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+#pragma unroll
+      for (int i = 0; i < 16; i++) s[j][i] = 0.0f;
+#pragma unroll
+      for (int n = 0; n < DP / 16; n++) {
+        const half8_t k = *reinterpret_cast<const half8_t *>(k_lds[b] + k_at + 32 * j * KS + 32 * n);
+#pragma unroll
+        for (int p = 0; p < NP; p++)
+          s[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[p][n], s[j], 0, 0, 0);
+      }
+    }
+  };
+  const auto scale_sums = [&](float f, int v_new) {
+    l *= f;
+    const float o = __builtin_ldexpf(f, v_ref - v_new);
+#pragma unroll
+    for (int t = 0; t < 2 * ND; t++)
+#pragma unroll
+      for (int i = 0; i < 16; i++) acc[t][i] *= o;
+  };
+  const auto raise = [&](float mx, int v_new) {
+    mx = swap_max32(mx);
+    const float m_new = fmaxf(m, mx);
+    if (__builtin_amdgcn_ballot_w64(m_new > m) != 0 || v_new != v_ref) {
+      scale_sums(m_new > m ? __builtin_amdgcn_exp2f(m - m_new) : 1.0f, v_new);
+      m = m_new;
+    }
+    return (m == kMinusInf ? 0.0f : m) - kWeightExponent;
+  };
+
+  const auto compute = [&](int b, const Staged (&st)[kWaves], int v_new) {
+    f32x16 s[2];
+    scores(b, s);
+    float c[kWaves], mx = kMinusInf;
+#pragma unroll
+    for (int n = 0; n < kWaves; n++) {
+      c[n] = __builtin_ldexpf(row_scale, st[n].k_ref() - X - 127);
+      float top;
+      if (st[n].missing()) {
+        top = kMinusInf;
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+          const float x = s[n >> 1][8 * (n & 1) + i];
+          const bool gone = powers[b][16 * n + 8 * (i >> 2) + 4 * half + (i & 3)] < 0.0f;
+          s[n >> 1][8 * (n & 1) + i] = gone ? kMinusInf : x;
+          top = gone ? top : fmaxf(top, x);
+        }
+        if (top != kMinusInf) top *= c[n];
+      } else {
+        top = s[n >> 1][8 * (n & 1)];
+#pragma unroll
+        for (int i = 1; i < 8; i++) top = fmaxf(top, s[n >> 1][8 * (n & 1) + i]);
+        top *= c[n];
+      }
+      mx = fmaxf(mx, top);
+    }
+    const float less = raise(mx, v_new);
+#pragma unroll
+    for (int n = 0; n < kWaves; n++) {
+      half8_t p[NP];
+      float e[8];
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        const float x = s[n >> 1][8 * (n & 1) + i];
+        e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x, c[n], -less));
+      }
+      if (st[n].missing()) {  // not -inf * c, where c is 0 or NaN
+#pragma unroll
+        for (int i = 0; i < 8; i++) e[i] = s[n >> 1][8 * (n & 1) + i] == kMinusInf ? 0.0f : e[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; i++) l += e[i];
+      const int lower = v_new - st[n].v_ref();
+      if (lower != 0) {
+        const float f = __builtin_ldexpf(1.0f, -lower);
+#pragma unroll
+        for (int i = 0; i < 8; i++) e[i] *= f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        p[0][i] = (_Float16)e[i];
+        if constexpr (NP == 2) p[1][i] = (_Float16)(e[i] - (float)p[0][i]);
+      }
+#pragma unroll
+      for (int t = 0; t < 2 * ND; t++) {
+        const half8_t v = __builtin_bit_cast(half8_t, value_operand(b, n, t));
+#pragma unroll
+        for (int k = 0; k < NP; k++)
+          acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p[k], acc[t], 0, 0, 0);
+      }
+    }
+  };
+
+  const auto compute_mixed = [&](int b, int first, bool nans) {
+    f32x16 s[2];
+    scores(b, s);
+    uint32_t sees = 0;
+    float mx = kMinusInf;
+#pragma unroll
+    for (int j = 0; j < 2; j++)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        const int at = 32 * j + 2 * i + 4 * half;
+        const f32x4 c = *reinterpret_cast<const f32x4 *>(&powers[b][at]);
+#pragma unroll
+        for (int n = 0; n < 4; n++) {
+          const int key = first + at + n;
+          const bool see = c[n] >= 0.0f && key >= mine.lo && key <= mine.hi;
+          s[j][i + n] = see ? s[j][i + n] * row_scale * c[n] : kMinusInf;
+          sees |= (see ? 1u : 0u) << (16 * j + i + n);
+          mx = fmaxf(mx, s[j][i + n]);
+        }
+      }
+    const float less = raise(mx, v_ref);
+    const float f = __builtin_ldexpf(1.0f, 127 + X - v_ref);  // values are not scaled here
+#pragma unroll
+    for (int n = 0; n < kWaves; n++) {
+      bf16x8 p[NP + 1];
+      half8_t seen;
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        float e = __builtin_amdgcn_exp2f(s[n >> 1][8 * (n & 1) + i] - less);
+        l += e;
+        e *= f;
+#pragma unroll
+        for (int k = 0; k <= NP; k++) {
+          p[k][i] = (__bf16)e;
+          e -= (float)p[k][i];
+        }
+        seen[i] = sees >> (8 * n + i) & 1 ? (_Float16)1.0f : (_Float16)0.0f;
+      }
+#pragma unroll
+      for (int t = 0; t < 2 * ND; t++) {
+        s16x8 v = value_operand(b, n, t);
+        f32x16 count;
+        if (nans) {
+          half8_t bad;
+#pragma unroll
+          for (int i = 0; i < 8; i++) {
+            const bool is = (v[i] & 0x7FFF) > 0x7F80;
+            bad[i] = is ? (_Float16)1.0f : (_Float16)0.0f;
+            v[i] = is ? (short)0 : v[i];
+          }
+#pragma unroll
+          for (int i = 0; i < 16; i++) count[i] = 0.0f;
+          count = __builtin_amdgcn_mfma_f32_32x32x16_f16(bad, seen, count, 0, 0, 0);
+        }
+#pragma unroll
+        for (int k = 0; k <= NP; k++)
+          acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v), p[k],
+                                                           acc[t], 0, 0, 0);
+        if (nans) {
+#pragma unroll
+          for (int i = 0; i < 16; i++)
+            if (count[i] > 0.0f) acc[t][i] = __builtin_nanf("");
+        }
+        __builtin_amdgcn_sched_barrier(0);  // or all operands are read at once
+      }
+    }
+  };
+
+  Data d;
+  load(w.first, d);
+  if (w.first < w.last) stage(w.first, d, k_ref, v_ref);
+  load(w.first + 1, d);
+  __syncthreads();
+  for (int t = w.first; t < w.last; t++) {
+    const int b = t & 1, first = w.begin + t * kTile;
+    const bool mixed = is_mixed(t);
+    Staged st[kWaves];
+    {
+      const u32x4 words = *reinterpret_cast<const u32x4 *>(&staged[b][0]);
+#pragma unroll
+      for (int n = 0; n < kWaves; n++)
+        st[n].word = (uint32_t)__builtin_amdgcn_readfirstlane((int)words[n]);
+    }
+    int k_new = k_ref, v_new = v_ref;
+    if (!mixed) {
+      k_new = max(max(st[0].k_ref(), st[1].k_ref()), max(st[2].k_ref(), st[3].k_ref()));
+      v_new = value_ref(v_ref, max(max(st[0].v_ref(), st[1].v_ref()), max(st[2].v_ref(), st[3].v_ref())));
+    }
+    if (t + 1 < w.last) {
+      stage(t + 1, d, k_new, v_new);
+      load(t + 2, d);
+    }
+    if (active && max(first, one.lo) <= min(first + kTile - 1, two.hi)) {
+      if (mixed) compute_mixed(b, first, (st[0].word | st[1].word | st[2].word | st[3].word) >> 17 & 1);
+      else compute(b, st, v_new);
+    } else if (v_new != v_ref) {
+      scale_sums(1.0f, v_new);
+    }
+    k_ref = k_new;
+    v_ref = v_new;
+    __syncthreads();
+  }
+
+  // the row's sums; a lane has dims 8 (i / 4) + 4 half + i % 4 of each 32
+  l = add_partner_row<64>(l);
+  const int out_row = w.r0 + 32 * wave + r32;
+  if (out_row > last_row) return;
+  const int head = w.kv_head * a.group + row - token * a.group;
+  const int64_t flat = (int64_t)(w.seq.q0 + token) * a.n_kv_heads * a.group + head;
+  const bool whole = w.splits == 1;
+  if (!whole && half == 0)
+    reinterpret_cast<float2 *>(a.partial + a.n_rows * a.splits * D)[flat * a.splits + w.split] =
+        make_float2(m, l);
+  const float inv = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+#pragma unroll
+  for (int t = 0; t < 2 * ND; t++)
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const int c = 32 * t + 2 * i + 4 * half;
+      f32x4 v;
+#pragma unroll
+      for (int n = 0; n < 4; n++) v[n] = __builtin_ldexpf(acc[t][i + n] * inv, v_ref - X - 127);
+      if (32 * t < D) {
+        if (whole) store_y4(a, (int64_t)(w.seq.q0 + token) * a.y_stride + (int64_t)head * D + c, v);
+        else *reinterpret_cast<f32x4 *>(a.partial + (flat * a.splits + w.split) * D + c) = v;
+      }
+    }
+}
+
+}  // namespace
+
+hipError_t attention_tiled_launch(const AttentionArgs &a, int blocks, hipStream_t stream) {
+  const int nd = (a.head_dim + 63) / 64;
+#define GO(NP, F, ND)                                                                     \
+  hipLaunchKernelGGL((attention_tiled_kernel<NP, F, ND>), dim3(blocks), dim3(kWaves * 64), 0, \
+                     stream, a)
+#define BY_DIM(NP, F)                    \
+  switch (nd) {                          \
+    case 1: GO(NP, F, 1); break;         \
+    case 2: GO(NP, F, 2); break;         \
+    case 3: GO(NP, F, 3); break;         \
+    default: GO(NP, F, 4); break;        \
+  }
+  if (a.type == MX_F32) {
+    if (a.format == MX_FP4) { BY_DIM(2, MX_FP4) } else { BY_DIM(2, MX_FP8) }
+  } else {
+    if (a.format == MX_FP4) { BY_DIM(1, MX_FP4) } else { BY_DIM(1, MX_FP8) }
+  }
+#undef BY_DIM
+#undef GO
+  return hipGetLastError();
+}
+
+}  // namespace q4k
