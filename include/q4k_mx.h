@@ -170,7 +170,7 @@ int mxfp4_moe(const void *x, int type, const void *router, const float *router_b
  *                       head_dim/2 (MX_FP4)] bytes, 16-byte aligned
  *   k_scales, v_scales  [n_pages][n_heads][page_size][head_dim/32] bytes
  * A token's slot is page * page_size + its place in the page.
- *   page_size  1 .. 65536; n_pages > 0; n_pages * page_size below 2^31
+ *   page_size  1 .. 65536; n_pages > 0; n_pages * n_heads * page_size below 2^31
  *   head_dim   a multiple of 32, at most 256
  * Rows of values have strides: row t of x is at x + t * x_stride values, its
  * heads one after the other from there; at least n_heads * head_dim, and so

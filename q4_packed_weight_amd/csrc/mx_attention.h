@@ -32,6 +32,7 @@ namespace q4k {
 typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short i16x2 __attribute__((ext_vector_type(2)));
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 
 constexpr float kMinusInf = -__builtin_inff();
@@ -50,6 +51,9 @@ struct Sequence {
   }
 };
 
+// Each share of keys has at least so many.
+constexpr int kMinKeys = 128;
+
 // Starts and counts as they should be, whatever they hold.
 __device__ __forceinline__ Sequence sequence_of(const AttentionArgs &a, int s) {
   Sequence r;
@@ -60,28 +64,119 @@ __device__ __forceinline__ Sequence sequence_of(const AttentionArgs &a, int s) {
   return r;
 }
 
-// Each range of keys has at least so many.
-constexpr int kMinKeys = 256;
+__device__ __forceinline__ uint32_t swap_max_u32(uint32_t v) {  // over lanes 16 and 32 apart
+  const auto x = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  const uint32_t x0 = x[0], x1 = x[1];
+  v = max(x0, x1);
+  const auto y = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  const uint32_t y0 = y[0], y1 = y[1];
+  return max(y0, y1);
+}
 
-// What one workgroup works on, in steps of KEYS keys: rows r0 .. of a sequence's (token, head of the
-// group) pairs and the steps of keys that any of them sees, or its share.
+// Sums over the lanes up to each: within rows of 16, then the rows' last ones.
+template <int CTRL, int ROWS> __device__ __forceinline__ uint32_t add_dpp(uint32_t v) {
+  return v + (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+  v = add_dpp<0x111, 0xF>(v);  // row_shr 1, 2, 4, 8
+  v = add_dpp<0x112, 0xF>(v);
+  v = add_dpp<0x114, 0xF>(v);
+  v = add_dpp<0x118, 0xF>(v);
+  v = add_dpp<0x142, 0xA>(v);  // row_bcast 15, 31
+  return add_dpp<0x143, 0xC>(v);
+}
+__device__ __forceinline__ uint32_t lane_value(uint32_t v, int lane) {
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
+}
+
+// What one workgroup works on, in steps of KEYS keys: rows r0 .. of a
+// sequence's (token, head of the group) pairs and the steps of keys that any of
+// them sees, or its share.  A unit is such a share, for all key heads.
 struct Work {
   Sequence seq;
-  int index, kv_head, r0, rows, split, splits;  // index of the sequence; splits: ranges in use
+  int index, kv_head, r0, rows, split, splits;  // index of the sequence; splits: shares in use
+  uint32_t unit;   // of share 0
   Range any, all;  // keys that one row at least sees, that all do
   int begin, first, last;  // key of step 0; this share's steps
 };
 
-template <int ROWS, int KEYS>
-__device__ __forceinline__ bool work_of(const AttentionArgs &a, uint32_t block, int splits, Work &w) {
-  uint32_t n = a.by_kv_heads.of(block);
+// The sequences' units lie one after the other: a sequence of `tiles` tiles whose
+// keys make `shares` shares at most has tiles * shares.  The shares' length is one
+// for the whole batch, so that about a.shares_wanted workgroups come out and none
+// works longer than the others.  Every wave finds its place for itself, 64
+// sequences at a time.  BY_TILE: `n` counts tiles, not units.
+template <int ROWS, int KEYS, bool BY_TILE>
+__device__ __forceinline__ bool find_work(const AttentionArgs &a, uint32_t n, Work &w, int &tile,
+                                          int &share) {
+  const int lane = threadIdx.x & 63;
+  const auto sizes = [&](int s, Sequence &q, uint32_t &tiles, uint32_t &steps) {
+    tiles = steps = 0;
+    if (s >= a.n_seqs) return;
+    q = sequence_of(a, s);
+    tiles = (q.nq * a.group + ROWS - 1) / ROWS;
+    const int most = a.window ? (int)min((int64_t)q.nk, (int64_t)a.window + a.max_queries + KEYS) : q.nk;
+    steps = (most + KEYS - 1) / KEYS;
+  };
+  Sequence q;
+  uint32_t tiles, steps, total = 0;
+  share = 0x7FFFFFFF;
+  if (a.shares_wanted > 0) {
+    for (int s = lane; s - lane < a.n_seqs; s += 64) {
+      sizes(s, q, tiles, steps);
+      total += lane_value(wave_scan(tiles * steps), 63);
+    }
+    share = max((int)(total / a.shares_wanted) + 1, kMinKeys / KEYS);
+  }
+  uint32_t units_before = 0, tiles_before = 0;
+  for (int s = lane; s - lane < a.n_seqs; s += 64) {
+    sizes(s, q, tiles, steps);
+    const uint32_t shares = a.shares_wanted > 0 ? max(1u, (steps + share - 1) / share) : 1;
+    const uint32_t units_to = units_before + wave_scan(tiles * shares);
+    const uint32_t tiles_to = BY_TILE ? tiles_before + wave_scan(tiles) : 0;
+    const uint64_t after = __builtin_amdgcn_ballot_w64((BY_TILE ? tiles_to : units_to) > n);
+    if (after != 0) {
+      const int at = __builtin_ctzll(after);
+      const uint32_t mine_shares = lane_value(shares, at), mine_tiles = lane_value(tiles, at);
+      const uint32_t first = lane_value(units_to, at) - mine_tiles * mine_shares;
+      if constexpr (BY_TILE) {
+        tile = n - (lane_value(tiles_to, at) - mine_tiles);
+        w.split = 0;
+      } else {
+        tile = (n - first) / mine_shares;
+        w.split = (n - first) - tile * mine_shares;
+      }
+      w.unit = first + tile * mine_shares;
+      tile = mine_tiles - 1 - tile;  // those with most keys first
+      w.index = s - lane + at;
+      w.seq.q0 = lane_value(q.q0, at);
+      w.seq.nq = lane_value(q.nq, at);
+      w.seq.total = lane_value(q.total, at);
+      w.seq.nk = lane_value(q.nk, at);
+      return true;
+    }
+    units_before = lane_value(units_to, 63);
+    if (BY_TILE) tiles_before = lane_value(tiles_to, 63);
+  }
+  return false;
+}
+
+// The work of a block; blocks count units (tiles) of all key heads, the heads of
+// one next to each other.
+template <int ROWS, int KEYS, bool BY_TILE = false>
+__device__ __forceinline__ bool work_of(const AttentionArgs &a, uint32_t block, Work &w) {
+  const uint32_t n = a.by_kv_heads.of(block);
   w.kv_head = block - n * a.n_kv_heads;
-  const uint32_t n2 = splits > 1 ? a.by_splits.of(n) : n;
-  w.split = n - n2 * splits;
-  const uint32_t s = a.by_tiles.of(n2);
-  w.index = s;
-  w.r0 = (a.tiles - 1 - (n2 - s * a.tiles)) * ROWS;  // those with most keys first
-  w.seq = sequence_of(a, s);
+  int tile, share = 0x7FFFFFFF;
+  if (a.planned) {
+    if (!find_work<ROWS, KEYS, BY_TILE>(a, n, w, tile, share)) return false;
+  } else {  // too many sequences to look through: as many tiles as the longest may have
+    w.index = a.by_tiles.of(n);
+    tile = a.tiles - 1 - (n - w.index * a.tiles);
+    w.split = 0;
+    w.unit = n;
+    w.seq = sequence_of(a, w.index);
+  }
+  w.r0 = tile * ROWS;
   const int all_rows = w.seq.nq * a.group;
   if (w.r0 >= all_rows) return false;
   w.rows = min(ROWS, all_rows - w.r0);
@@ -91,11 +186,20 @@ __device__ __forceinline__ bool work_of(const AttentionArgs &a, uint32_t block, 
   w.all = {two.lo, one.hi};
   w.begin = w.any.lo & ~(KEYS - 1);
   const int steps = w.any.hi < w.any.lo ? 0 : (w.any.hi + KEYS - w.begin) / KEYS;
-  w.splits = min(a.splits, max(1, steps / (kMinKeys / KEYS)));
-  const int share = (steps + w.splits - 1) / w.splits;
+  share = min(share, max(steps, 1));
+  w.splits = max(1, (steps + share - 1) / share);
   w.first = w.split * share;
   w.last = min(steps, w.first + share);
-  return true;
+  return w.split < w.splits;
+}
+
+// Where a row of a share has its part: rows, then rows' largest x and sums.
+template <int ROWS>
+__device__ __forceinline__ int64_t part_row(const AttentionArgs &a, const Work &w, int share, int row) {
+  return ((int64_t)(w.unit + share) * a.n_kv_heads + w.kv_head) * ROWS + row;
+}
+__device__ __forceinline__ float2 *part_stats(const AttentionArgs &a) {
+  return reinterpret_cast<float2 *>(a.partial + a.n_parts * a.head_dim);
 }
 
 __device__ __forceinline__ float swap_max16(float v) {
@@ -109,15 +213,6 @@ __device__ __forceinline__ float swap_max32(float v) {
   const auto h = __builtin_amdgcn_permlane32_swap(b, b, false, false);
   const uint32_t x = h[0], y = h[1];
   return fmaxf(__uint_as_float(x), __uint_as_float(y));
-}
-
-__device__ __forceinline__ uint32_t swap_max_u32(uint32_t v) {  // over lanes 16 and 32 apart
-  const auto x = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-  const uint32_t x0 = x[0], x1 = x[1];
-  v = max(x0, x1);
-  const auto y = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-  const uint32_t y0 = y[0], y1 = y[1];
-  return max(y0, y1);
 }
 
 __device__ __forceinline__ uint32_t pk_max(uint32_t a, uint32_t b) {
@@ -184,6 +279,45 @@ template <int W> __device__ __forceinline__ void load_codes(const uint8_t *p, ui
   }
 }
 
+// The scale bytes of a lane's blocks 2 p + g / 2 of a row: as loaded (whole
+// dwords of four blocks where rows are made of them, else bytes), and, once
+// settled, two to a dword.
+struct __attribute__((packed)) Packed4 { uint32_t v; };  // at any alignment
+template <int ND> struct RawScales {
+  static constexpr int S = (ND + 1) / 2;
+  uint32_t raw[ND], pair[S];
+  __device__ __forceinline__ void load(const uint8_t *row, int nb, int g, bool fours) {
+    if (fours) {
+#pragma unroll
+      for (int i = 0; i < ND; i++)
+        raw[i] = i & 1 ? 0 : reinterpret_cast<const Packed4 *>(row + 2 * i)->v;
+    } else {
+#pragma unroll
+      for (int p = 0; p < ND; p++) raw[p] = row[min(2 * p + (g >> 1), nb - 1)];
+    }
+  }
+  __device__ __forceinline__ void settle(int g, bool fours) {
+#pragma unroll
+    for (int i = 0; i < S; i++) {
+      const uint32_t bytes = 2 * i + 1 < ND ? raw[2 * i] | raw[2 * i + 1 < ND ? 2 * i + 1 : 0] << 16 : raw[2 * i];
+      pair[i] = fours ? raw[2 * i] >> (8 * (g >> 1)) & 0x00FF00FFu : bytes;
+    }
+  }
+  // 2^(s + base - 127), s + base <= 254; NaN blocks as any others
+  __device__ __forceinline__ void powers(int base, float (&f)[ND]) const {
+    const i16x2 add = {(short)base, (short)base}, none = {0, 0};
+#pragma unroll
+    for (int i = 0; i < S; i++) {
+      const uint32_t e = __builtin_bit_cast(
+          uint32_t, __builtin_elementwise_max(__builtin_bit_cast(i16x2, pair[i]) + add, none));
+      f[2 * i] = __builtin_bit_cast(float, e << 23);
+      if (2 * i + 1 < ND) f[2 * i + 1 < ND ? 2 * i + 1 : 0] = __builtin_bit_cast(float, (e & 0xFFFF0000u) << 7);
+    }
+  }
+  __device__ __forceinline__ void clear(int p) { pair[p / 2] &= p & 1 ? 0x0000FFFFu : 0xFFFF0000u; }
+  __device__ __forceinline__ uint32_t of(int p) const { return pair[p / 2] >> (16 * (p & 1)) & 0xFFFF; }
+};
+
 template <int FMT>
 __device__ __forceinline__ bf16x8 codes_operand_bf16(const uint32_t *c, float scale) {
   bf16x2 h0, h1, h2, h3;
@@ -211,14 +345,22 @@ __device__ __forceinline__ bool has_nan(const uint32_t (&c)[W], uint32_t s) {
   return r;
 }
 
-// Eight consecutive values of a row of q.
-__device__ __forceinline__ void load_q8(const AttentionArgs &a, int64_t at, float (&f)[8]) {
-  if (a.type == MX_F32)
-    raw8_to_f32<MX_F32>(load_raw8<MX_F32>(static_cast<const float *>(a.q) + at, 0), f);
-  else if (a.type == MX_BF16)
-    raw8_to_f32<MX_BF16>(load_raw8<MX_BF16>(static_cast<const __bf16 *>(a.q) + at, 0), f);
-  else
-    raw8_to_f32<MX_F16>(load_raw8<MX_F16>(static_cast<const _Float16 *>(a.q) + at, 0), f);
+// Eight consecutive values of a row of q, as they lie in memory and in fp32: NP
+// = 2 stands for fp32, one operand for the 16-bit types.  No branch lies
+// between loads, so that all are on their way together.
+template <int NP> struct RawQ { Raw8<NP == 2 ? MX_F32 : MX_F16> v; };
+template <int NP> __device__ __forceinline__ RawQ<NP> load_q8(const AttentionArgs &a, int64_t at) {
+  return {load_raw8<NP == 2 ? MX_F32 : MX_F16>(static_cast<const uint8_t *>(a.q) + at * (2 * NP), 0)};
+}
+template <int NP>
+__device__ __forceinline__ void q8_to_f32(const AttentionArgs &a, const RawQ<NP> &r, float (&f)[8]) {
+  if constexpr (NP == 2) {
+    raw8_to_f32<MX_F32>(r.v, f);
+  } else if (a.type == MX_BF16) {
+    raw8_to_f32<MX_BF16>({r.v.v}, f);
+  } else {
+    raw8_to_f32<MX_F16>(r.v, f);
+  }
 }
 
 __device__ __forceinline__ void store_y4(const AttentionArgs &a, int64_t at, f32x4 v) {

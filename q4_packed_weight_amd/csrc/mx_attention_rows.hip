@@ -1,5 +1,7 @@
 // mx_attention_rows.hip -- attention over a paged MX cache for few rows: the
 // (token, head) pairs of one key head's group, 16 at a time.
+#include <algorithm>
+
 #include "mx_attention.h"
 
 namespace q4k {
@@ -14,19 +16,26 @@ constexpr int kStepKeys = 32;
 template <int FMT, int ND> struct StepData {
   static constexpr int W = FMT == MX_FP8 ? 4 : 2;  // dwords of 16 codes
   uint32_t k[2][ND][W], v[2][ND][W];
-  uint32_t ks[2][ND], vs[2][ND];
+  RawScales<ND> ks[2], vs[2];
   uint32_t ok;  // bit by key, the same in every lane
 };
+
+// Waves that a SIMD holds at a time: as many as keep a lane's registers (codes,
+// queries, sums) from memory.
+template <int NP, int ND>
+constexpr int kWavesPerSimd = ND == 1 ? 5 : ND == 2 ? (NP == 1 ? 4 : 3) : ND == 3 ? 2 : 1;
 
 // Scores are products S^T = K Q^T of 16 keys by 16 rows: a lane's result is of
 // its row l % 16 and keys 4g .. 4g+3, so that a row's statistics are a lane's
 // own, and after exp2 the eight weights of two tiles are, as they stand, the
 // operand of O^T += V^T P^T with the keys in that order.  V goes through LDS
 // as fp16, each wave its own 32 keys, and comes back transposed.  A wave takes
-// every fourth step of its workgroup's range, the next one's codes in flight;
-// the four results, and those of the ranges, are joined by their largest x.
-template <int NP, int FMT, int ND>
-__global__ __launch_bounds__(kWaves * 64) void attention_rows_kernel(AttentionArgs a) {
+// every fourth step of its workgroup's range; once a step's codes are operands
+// and in LDS, the next one's are sent for, and its weights and sums are made
+// while they come.  The four results, and those of the ranges, are joined by
+// their largest x.
+template <int NP, int FMT, int ND, bool MIXED>
+__global__ __launch_bounds__(kWaves * 64, MIXED ? 1 : (kWavesPerSimd<NP, ND>)) void attention_rows_kernel(AttentionArgs a) {
   constexpr int DP = 64 * ND;                // dims, padded
   constexpr int VS = 2 * DP + 32;            // bytes of a key's row of V in LDS
   constexpr int OS = DP + 4;                 // floats of a row of the result
@@ -35,7 +44,7 @@ __global__ __launch_bounds__(kWaves * 64) void attention_rows_kernel(AttentionAr
   __shared__ float2 stats[kWaves][kRows];
   __shared__ __attribute__((aligned(16))) float powers[kWaves][kStepKeys];
   Work w;
-  if (!work_of<kRows, kStepKeys>(a, blockIdx.x, a.splits, w) || w.split >= w.splits) return;
+  if (!work_of<kRows, kStepKeys>(a, blockIdx.x, w)) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
   const int D = a.head_dim, nb = D / 32;
   const int64_t code_row = FMT == MX_FP8 ? D : D / 2;
@@ -43,22 +52,94 @@ __global__ __launch_bounds__(kWaves * 64) void attention_rows_kernel(AttentionAr
 #pragma unroll
   for (int p = 0; p < ND; p++) has[p] = 64 * p + 16 * g < D;
 
+  const int32_t *const table = a.table + (int64_t)w.index * a.pages_per_seq;
+  // pages of a step's keys; those of keys that no row sees are not used
+  const auto load_pages = [&](int step, int (&page)[2]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+      const int key = w.begin + step * kStepKeys + 16 * j + r16;
+      page[j] = table[a.by_page.of(min(max(key, w.any.lo), w.any.hi))];
+    }
+  };
+  int pages[2];
+  if (w.first + wave < w.last) load_pages(w.first + wave, pages);
+
   // queries: rows behind the last one are its copies
   const int row = w.r0 + min(r16, w.rows - 1);
   const int token = a.by_group.of(row);
   const Range mine = w.seq.sees(a, token);
-  half8_t q[NP][ND][2];
-  float row_scale;
+  RawQ<NP> raw[ND][2];
   {
     const int64_t at = (int64_t)(w.seq.q0 + token) * a.q_stride +
                        (int64_t)(w.kv_head * a.group + row - token * a.group) * D;
+#pragma unroll
+    for (int p = 0; p < ND; p++)
+#pragma unroll
+      for (int h = 0; h < 2; h++) raw[p][h] = load_q8<NP>(a, at + (has[p] ? 64 * p + 16 * g : 0) + 8 * h);
+  }
+  // Every lane loads, absent keys and dims row 0 of their head and dims 0 of
+  // their row, without a branch; fill_in puts zeros there.
+  const bool odd = (D & 32) != 0, fours = nb % 4 == 0;
+  StepData<FMT, ND> d;
+  const auto load_step = [&](int step, const int (&page)[2]) __attribute__((always_inline)) {
+    uint32_t okay = 0;
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+      const int key = w.begin + step * kStepKeys + 16 * j + r16;
+      const bool ok = step < w.last && key >= w.any.lo && key <= w.any.hi &&
+                      (uint32_t)page[j] < (uint32_t)a.n_pages;
+      okay |= ((uint32_t)__builtin_amdgcn_ballot_w64(ok) & 0xFFFFu) << (16 * j);
+      const uint32_t place = key - a.by_page.of(key) * a.page_size;
+      const uint32_t r = ok ? (page[j] * a.n_kv_heads + w.kv_head) * a.page_size + place : 0;
+      const uint64_t at = (uint64_t)r * code_row, s_at = (uint64_t)r * nb;
+#pragma unroll
+      for (int p = 0; p < ND; p++) {
+        const int c = (has[p] ? 64 * p + 16 * g : 0) * (FMT == MX_FP8 ? 2 : 1) / 2;
+        load_codes(a.k_codes + at + c, d.k[j][p]);
+        load_codes(a.v_codes + at + c, d.v[j][p]);
+      }
+      d.ks[j].load(a.k_scales + s_at, nb, g, fours);
+      d.vs[j].load(a.v_scales + s_at, nb, g, fours);
+    }
+    d.ok = (uint32_t)__builtin_amdgcn_readfirstlane((int)okay);
+  };
+  const auto fill_in = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+      d.ks[j].settle(g, fours);
+      d.vs[j].settle(g, fours);
+    }
+    if (d.ok != 0xFFFFFFFFu || odd) {
+#pragma unroll
+      for (int j = 0; j < 2; j++) {
+        const bool ok = d.ok >> (16 * j + r16) & 1;
+#pragma unroll
+        for (int p = 0; p < ND; p++) {
+          if (!ok || !has[p]) {
+#pragma unroll
+            for (int i = 0; i < StepData<FMT, ND>::W; i++) d.k[j][p][i] = d.v[j][p][i] = 0;
+            d.ks[j].clear(p);
+            d.vs[j].clear(p);
+          }
+        }
+      }
+    }
+  };
+
+  if (w.first + wave < w.last) {
+    load_step(w.first + wave, pages);
+    load_pages(w.first + wave + kWaves, pages);
+  }
+  half8_t q[NP][ND][2];
+  float row_scale;
+  {
     float f[ND][2][8];
     uint32_t amax = 0;
 #pragma unroll
     for (int p = 0; p < ND; p++)
 #pragma unroll
       for (int h = 0; h < 2; h++) {
-        if (has[p]) load_q8(a, at + 64 * p + 16 * g + 8 * h, f[p][h]);
+        q8_to_f32<NP>(a, raw[p][h], f[p][h]);
 #pragma unroll
         for (int i = 0; i < 8; i++) {
           if (!has[p]) f[p][h][i] = 0.0f;
@@ -81,40 +162,6 @@ __global__ __launch_bounds__(kWaves * 64) void attention_rows_kernel(AttentionAr
         }
   }
 
-  const int32_t *const table = a.table + (int64_t)w.index * a.pages_per_seq;
-  const auto load_step = [&](int step, StepData<FMT, ND> &d) {
-    uint32_t okay = 0;
-#pragma unroll
-    for (int j = 0; j < 2; j++) {
-      const int key = w.begin + step * kStepKeys + 16 * j + r16;
-      bool ok = step < w.last && key >= w.any.lo && key <= w.any.hi;
-      int page = 0, at = 0;
-      if (ok) {
-        at = a.by_page.of(key);
-        page = table[at];
-        ok = page >= 0 && page < a.n_pages;
-      }
-      const int64_t r = ((int64_t)page * a.n_kv_heads + w.kv_head) * a.page_size +
-                        (key - at * a.page_size);
-      okay |= ((uint32_t)__builtin_amdgcn_ballot_w64(ok) & 0xFFFFu) << (16 * j);
-#pragma unroll
-      for (int p = 0; p < ND; p++) {
-        d.ks[j][p] = d.vs[j][p] = 0;
-#pragma unroll
-        for (int i = 0; i < StepData<FMT, ND>::W; i++) d.k[j][p][i] = d.v[j][p][i] = 0;
-        if (ok && has[p]) {
-          const int64_t c = r * code_row + (64 * p + 16 * g) * (FMT == MX_FP8 ? 2 : 1) / 2;
-          const int64_t s = r * nb + 2 * p + (g >> 1);
-          load_codes(a.k_codes + c, d.k[j][p]);
-          load_codes(a.v_codes + c, d.v[j][p]);
-          d.ks[j][p] = a.k_scales[s];
-          d.vs[j][p] = a.v_scales[s];
-        }
-      }
-    }
-    d.ok = (uint32_t)__builtin_amdgcn_readfirstlane((int)okay);
-  };
-
   f32x4 acc[4 * ND];
 #pragma unroll
   for (int i = 0; i < 4 * ND; i++) acc[i] = f32x4{0, 0, 0, 0};
@@ -127,22 +174,21 @@ __global__ __launch_bounds__(kWaves * 64) void attention_rows_kernel(AttentionAr
   constexpr int W = StepData<FMT, ND>::W;
 
   // 16 dims of 32 values, transposed
-  const auto value_operand = [&](int t) {
+  const auto value_operand = [&](int t) __attribute__((always_inline)) {
     const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsS16x4 *)(read_at + 32 * t));
     const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsS16x4 *)(read_at + 32 * t + 16 * VS));
     return s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
   };
-  // scores of the step's keys under the scales that `base(j)` gives tile j
-  const auto scores = [&](const StepData<FMT, ND> &d, const auto &base, f32x4 (&s)[2]) {
+  // scores of the step's keys, their blocks scaled by f
+  const auto scores = [&](const float (&f)[2][ND], f32x4 (&s)[2]) __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < 2; j++) {
       s[j] = f32x4{0, 0, 0, 0};
 #pragma unroll
       for (int p = 0; p < ND; p++) {
-        const float f = block_scale(d.ks[j][p], base(j));
 #pragma unroll
         for (int h = 0; h < 2; h++) {
-          const half8_t k = codes_operand<FMT>(&d.k[j][p][h * W / 2], f);
+          const half8_t k = codes_operand<FMT>(&d.k[j][p][h * W / 2], f[j][p]);
 #pragma unroll
           for (int n = 0; n < NP; n++)
             s[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[n][p][h], s[j], 0, 0, 0);
@@ -150,56 +196,95 @@ __global__ __launch_bounds__(kWaves * 64) void attention_rows_kernel(AttentionAr
       }
     }
   };
-  // the values of x go into the maximum; what was summed is scaled to the new one
-  // and to the new reference
-  const auto raise = [&](const float (&x)[8], int v_new) {
+  // The values of x go into the maximum, and what was summed is scaled to the new
+  // one and to the new reference; a maximum that is up to 2^4 too low stays, as
+  // the weights' 2^14 still are fp16.
+  const auto raise = [&](const float (&x)[8], int v_new) __attribute__((always_inline)) {
     float mx = x[0];
 #pragma unroll
     for (int i = 1; i < 8; i++) mx = fmaxf(mx, x[i]);
     mx = swap_max32(swap_max16(mx));
-    const float m_new = fmaxf(m, mx);
-    if (__builtin_amdgcn_ballot_w64(m_new > m) != 0 || v_new != v_ref) {
-      const float f = m_new > m ? __builtin_amdgcn_exp2f(m - m_new) : 1.0f;
+    const bool up = mx > m + 4.0f;
+    if (__builtin_amdgcn_ballot_w64(up) != 0 || v_new != v_ref) {
+      const float f = up ? __builtin_amdgcn_exp2f(m - mx) : 1.0f;
       l *= f;
       const float o = __builtin_ldexpf(f, v_ref - v_new);
 #pragma unroll
       for (int i = 0; i < 4 * ND; i++) acc[i] *= o;
-      m = m_new;
+      m = up ? mx : m;
       v_ref = v_new;
     }
     return (m == kMinusInf ? 0.0f : m) - kWeightExponent;
   };
 
-  // keys that all rows see (or none: absent ones)
-  const auto compute = [&](const StepData<FMT, ND> &d) {
-    uint32_t top = 0;
+  // Keys that all rows see (or none: absent ones).  The references stay as long
+  // as no scale of the step is above them and one at least is no more than 2^8
+  // below, which each lane compares for itself; else they are made anew.
+  int k_ref = kFirstValueRef;
+  const auto compute = [&](int step) __attribute__((always_inline)) {
+    uint32_t k_top = 0, v_top = 0;
 #pragma unroll
     for (int j = 0; j < 2; j++)
 #pragma unroll
-      for (int p = 0; p < ND; p++)
-        top = pk_max(top, scale_rank(d.ks[j][p]) | scale_rank(d.vs[j][p]) << 16);
-    top = wave_pk_max(top);
-    const int k_ref = top & 0xFFFF, v_new = value_ref(v_ref, (int)(top >> 16));
+      for (int p = 0; p < d.ks[j].S; p++) {
+        k_top = pk_max(k_top, d.ks[j].pair[p]);
+        v_top = pk_max(v_top, d.vs[j].pair[p]);
+      }
+    k_top = max(k_top & 0xFFFF, k_top >> 16);
+    v_top = max(v_top & 0xFFFF, v_top >> 16);
+    int v_new = v_ref;
+    bool nans = false;
+    if (__builtin_amdgcn_ballot_w64((int)k_top > k_ref || (int)v_top > v_ref) != 0 ||
+        __builtin_amdgcn_ballot_w64((int)k_top + 8 >= k_ref) == 0 ||
+        __builtin_amdgcn_ballot_w64((int)v_top + 8 >= v_ref) == 0) {
+      nans = __builtin_amdgcn_ballot_w64(max(k_top, v_top) == 255) != 0;
+      uint32_t top = 0;
+#pragma unroll
+      for (int j = 0; j < 2; j++)
+#pragma unroll
+        for (int p = 0; p < ND; p++)
+          top = pk_max(top, scale_rank(d.ks[j].of(p)) | scale_rank(d.vs[j].of(p)) << 16);
+      top = wave_pk_max(top);
+      k_ref = value_ref(k_ref, (int)(top & 0xFFFF));
+      v_new = value_ref(v_ref, (int)(top >> 16));
+    }
+    float kf[2][ND], vf[2][ND];
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+      d.ks[j].powers(127 + X - k_ref, kf[j]);
+      d.vs[j].powers(127 + X - v_new, vf[j]);
+    }
+    if (nans) {
+#pragma unroll
+      for (int j = 0; j < 2; j++)
+#pragma unroll
+        for (int p = 0; p < ND; p++) {
+          if (d.ks[j].of(p) == 255) kf[j][p] = __builtin_nanf("");
+          if (d.vs[j].of(p) == 255) vf[j][p] = __builtin_nanf("");
+        }
+    }
 #pragma unroll
     for (int j = 0; j < 2; j++)
 #pragma unroll
       for (int p = 0; p < ND; p++) {
-        const float s = block_scale(d.vs[j][p], 127 + X - v_new);
         uint8_t *const to = mem + (16 * j + r16) * VS + (64 * p + 16 * g) * 2;
-        *reinterpret_cast<half8_t *>(to) = codes_operand<FMT>(&d.v[j][p][0], s);
-        *reinterpret_cast<half8_t *>(to + 16) = codes_operand<FMT>(&d.v[j][p][W / 2], s);
+        *reinterpret_cast<half8_t *>(to) = codes_operand<FMT>(&d.v[j][p][0], vf[j][p]);
+        *reinterpret_cast<half8_t *>(to + 16) = codes_operand<FMT>(&d.v[j][p][W / 2], vf[j][p]);
       }
     __builtin_amdgcn_wave_barrier();
     f32x4 s[2];
-    scores(d, [&](int) { return 127 + X - k_ref; }, s);
+    scores(kf, s);
+    const uint32_t ok = d.ok;
+    load_step(step + kWaves, pages);
+    load_pages(step + 2 * kWaves, pages);
     const float c = __builtin_ldexpf(row_scale, k_ref - X - 127);
     float x[8];
 #pragma unroll
     for (int i = 0; i < 8; i++) x[i] = s[i >> 2][i & 3] * c;
-    if (d.ok != 0xFFFFFFFFu) {
+    if (ok != 0xFFFFFFFFu) {
 #pragma unroll
       for (int i = 0; i < 8; i++)
-        x[i] = d.ok >> (16 * (i >> 2) + 4 * g + (i & 3)) & 1 ? x[i] : kMinusInf;
+        x[i] = ok >> (16 * (i >> 2) + 4 * g + (i & 3)) & 1 ? x[i] : kMinusInf;
     }
     const float less = raise(x, v_new);
     half8_t p[NP];
@@ -222,7 +307,7 @@ __global__ __launch_bounds__(kWaves * 64) void attention_rows_kernel(AttentionAr
 
   // keys that some rows see and others do not: no reference may come from a key
   // that a row does not see, and no NaN
-  const auto compute_mixed = [&](int step, const StepData<FMT, ND> &d) {
+  const auto compute_mixed = [&](int step) __attribute__((always_inline)) {
     uint32_t rank[2];
     bool nan = false;
 #pragma unroll
@@ -230,9 +315,9 @@ __global__ __launch_bounds__(kWaves * 64) void attention_rows_kernel(AttentionAr
       rank[j] = 0;
 #pragma unroll
       for (int p = 0; p < ND; p++) {
-        rank[j] = max(rank[j], scale_rank(d.ks[j][p]));
-        nan |= has_nan<FMT>(d.v[j][p], d.vs[j][p]);
-        const float s = block_scale(d.vs[j][p], 127 + X - v_ref);
+        rank[j] = max(rank[j], scale_rank(d.ks[j].of(p)));
+        nan |= has_nan<FMT>(d.v[j][p], d.vs[j].of(p));
+        const float s = block_scale(d.vs[j].of(p), 127 + X - v_ref);
         uint8_t *const to = mem + (16 * j + r16) * VS + (64 * p + 16 * g) * 2;
         *reinterpret_cast<bf16x8 *>(to) = codes_operand_bf16<FMT>(&d.v[j][p][0], s);
         *reinterpret_cast<bf16x8 *>(to + 16) = codes_operand_bf16<FMT>(&d.v[j][p][W / 2], s);
@@ -241,8 +326,16 @@ __global__ __launch_bounds__(kWaves * 64) void attention_rows_kernel(AttentionAr
       if (g == 0) powers[wave][16 * j + r16] = __builtin_ldexpf(1.0f, (int)rank[j] - X - 127);
     }
     __builtin_amdgcn_wave_barrier();
+    float kf[2][ND];
+#pragma unroll
+    for (int j = 0; j < 2; j++)
+#pragma unroll
+      for (int p = 0; p < ND; p++) kf[j][p] = block_scale(d.ks[j].of(p), 127 + X - (int)rank[j]);
     f32x4 s[2];
-    scores(d, [&](int j) { return 127 + X - (int)rank[j]; }, s);
+    scores(kf, s);
+    const uint32_t ok = d.ok;
+    load_step(step + kWaves, pages);
+    load_pages(step + 2 * kWaves, pages);
     const int first = w.begin + step * kStepKeys;
     float x[8];
     half8_t sees;
@@ -252,7 +345,7 @@ __global__ __launch_bounds__(kWaves * 64) void attention_rows_kernel(AttentionAr
 #pragma unroll
       for (int i = 0; i < 4; i++) {
         const int n = 16 * j + 4 * g + i, key = first + n;
-        const bool see = (d.ok >> n & 1) != 0 && key >= mine.lo && key <= mine.hi;
+        const bool see = (ok >> n & 1) != 0 && key >= mine.lo && key <= mine.hi;
         x[4 * j + i] = see ? s[j][i] * row_scale * c[i] : kMinusInf;
         sees[4 * j + i] = see ? (_Float16)1.0f : (_Float16)0.0f;
       }
@@ -299,25 +392,13 @@ __global__ __launch_bounds__(kWaves * 64) void attention_rows_kernel(AttentionAr
     }
     __builtin_amdgcn_wave_barrier();
   };
-  const auto take = [&](int step, const StepData<FMT, ND> &d) {
+  for (int step = w.first + wave; step < w.last; step += kWaves) {
+    fill_in();
     const int one = w.begin + step * kStepKeys;
-    if (max(one, w.any.lo) < w.all.lo || min(one + kStepKeys - 1, w.any.hi) > w.all.hi)
-      compute_mixed(step, d);
+    if (MIXED && (max(one, w.any.lo) < w.all.lo || min(one + kStepKeys - 1, w.any.hi) > w.all.hi))
+      compute_mixed(step);
     else
-      compute(d);
-  };
-
-  StepData<FMT, ND> d0, d1;
-  int step = w.first + wave;
-  load_step(step, d0);
-  while (step < w.last) {
-    load_step(step + kWaves, d1);
-    take(step, d0);
-    step += kWaves;
-    if (step >= w.last) break;
-    load_step(step + kWaves, d0);
-    take(step, d1);
-    step += kWaves;
+      compute(step);
   }
 
   // the waves' results, each as it stands before its power is put back
@@ -345,11 +426,9 @@ __global__ __launch_bounds__(kWaves * 64) void attention_rows_kernel(AttentionAr
   }
   const int out_row = w.r0 + out, out_token = a.by_group.of(out_row);
   const int head = w.kv_head * a.group + out_row - out_token * a.group;
-  const int64_t flat = (int64_t)(w.seq.q0 + out_token) * a.n_kv_heads * a.group + head;
   const bool whole = w.splits == 1;
-  if (!whole && (threadIdx.x & 15) == 0)
-    reinterpret_cast<float2 *>(a.partial + a.n_rows * a.splits * D)[flat * a.splits + w.split] =
-        make_float2(most, sum);
+  const int64_t part = part_row<kRows>(a, w, w.split, out);
+  if (!whole && (threadIdx.x & 15) == 0) part_stats(a)[part] = make_float2(most, sum);
   for (int c = 4 * (threadIdx.x & 15); c < D; c += 64) {
     f32x4 v = {0, 0, 0, 0};
 #pragma unroll
@@ -359,65 +438,114 @@ __global__ __launch_bounds__(kWaves * 64) void attention_rows_kernel(AttentionAr
       v *= sum == 0.0f ? 0.0f : 1.0f / sum;
       store_y4(a, (int64_t)(w.seq.q0 + out_token) * a.y_stride + (int64_t)head * D + c, v);
     } else {
-      *reinterpret_cast<f32x4 *>(a.partial + (flat * a.splits + w.split) * D + c) = v;
+      *reinterpret_cast<f32x4 *>(a.partial + part * D + c) = v;
     }
   }
 }
 
-// The ranges' results joined, a row to 16 lanes.
+// The shares' results joined, a wave to a row: the weights of 64 shares at a
+// time, then four dims of every second share to a lane (of all for head_dim
+// above 128, of every fourth up to 64).
 template <int ROWS, int KEYS>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a) {
+  constexpr int kChunk = ROWS == kRows ? 4 : 16;  // rows of a workgroup
   Work w;
-  if (!work_of<ROWS, KEYS>(a, blockIdx.x, 1, w) || w.splits == 1) return;
-  const int out = 16 * blockIdx.y + (threadIdx.x >> 4), D = a.head_dim;
-  if (out >= w.rows) return;
-  const int row = w.r0 + out, token = a.by_group.of(row);
-  const int head = w.kv_head * a.group + row - token * a.group;
-  const int64_t flat = (int64_t)(w.seq.q0 + token) * a.n_kv_heads * a.group + head;
-  const float2 *const stats =
-      reinterpret_cast<const float2 *>(a.partial + a.n_rows * a.splits * D) + flat * a.splits;
-  float most = kMinusInf, sum = 0.0f;
-  for (int i = 0; i < w.splits; i++) most = fmaxf(most, stats[i].x);
-  for (int i = 0; i < w.splits; i++) sum += part_share(stats[i].x, most) * stats[i].y;
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  for (int c = 4 * (threadIdx.x & 15); c < D; c += 64) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, D = a.head_dim;
+  if (!work_of<ROWS, KEYS, true>(a, blockIdx.x, w) || w.splits == 1 ||
+      w.unit + w.splits > a.units)  // starts that are not ascending
+    return;
+  const int width = D > 128 ? 64 : D > 64 ? 32 : 16, groups = 64 / width;
+  const int c = lane & (width - 1), g = lane / width, columns = D / 4;
+  const int64_t stride = (int64_t)a.n_kv_heads * ROWS;
+  for (int r = kChunk * blockIdx.y + wave; r < min(w.rows, kChunk * ((int)blockIdx.y + 1)); r += 4) {
+    const int row = w.r0 + r, token = a.by_group.of(row);
+    const int head = w.kv_head * a.group + row - token * a.group;
+    const int64_t part = part_row<ROWS>(a, w, 0, r);
+    const float2 *const stats = part_stats(a) + part;
+    const f32x4 *const values = reinterpret_cast<const f32x4 *>(a.partial + part * D) + c;
+    float m = kMinusInf, total = 0.0f;
     f32x4 v = {0, 0, 0, 0};
-    for (int i = 0; i < w.splits; i++)
-      v += part_share(stats[i].x, most) *
-           *reinterpret_cast<const f32x4 *>(a.partial + (flat * a.splits + i) * D + c);
-    store_y4(a, (int64_t)(w.seq.q0 + token) * a.y_stride + (int64_t)head * D + c, v * inv);
+    for (int from = 0; from < w.splits; from += 64) {
+      const int n = min(64, w.splits - from);
+      const float2 mine = lane < n ? stats[(from + lane) * stride] : make_float2(kMinusInf, 0.0f);
+      float most = mine.x;
+#pragma unroll
+      for (int i = 1; i < 64; i *= 2) most = fmaxf(most, __shfl_xor(most, i));
+      most = fmaxf(most, m);
+      const float share = part_share(mine.x, most), before = part_share(m, most);
+      total = total * before + group_sum<64>(share * mine.y);
+      v *= before;
+      for (int i = 0; i < n; i += groups) {
+        const float f = __shfl(share, (i + g) & 63);
+        if (i + g < n && c < columns) v += f * values[(from + i + g) * stride * columns];
+      }
+      m = most;
+    }
+    for (int i = width; i < 64; i *= 2) {
+#pragma unroll
+      for (int k = 0; k < 4; k++) v[k] += __shfl_xor(v[k], i);
+    }
+    if (g == 0 && c < columns)
+      store_y4(a, (int64_t)(w.seq.q0 + token) * a.y_stride + (int64_t)head * D + 4 * c,
+               v * (total == 0.0f ? 0.0f : 1.0f / total));
   }
 }
 
 // More than one tile of 16 rows: the form for many rows.
 bool tiled(const AttentionArgs &a) { return (int64_t)a.max_queries * a.group > kRows; }
 
+// Workgroups on the chip at a time.
+int slots(const AttentionArgs &a) {
+  const int nd = (a.head_dim + 63) / 64;
+  if (tiled(a)) return 256 * (nd <= 2 ? 2 : 1);
+  return 256 * (nd <= 2 ? 4 : 2);
+}
+constexpr int kMaxPlanned = 512;  // sequences that every workgroup looks through
+
 }  // namespace
 
-// Ranges of keys so that about four workgroups come to a CU, none for fewer
-// than kMinKeys keys.
+// Tiles are laid out by the sequences' own sizes where those are few enough to
+// look through; keys are cut into shares where the tiles alone are fewer than
+// twice (many rows: once) the workgroups that run at a time.
 int64_t mx_attention_workspace_bytes(AttentionArgs &a) {
-  const int rows = tiled(a) ? kTiledRows : kRows;
+  const int rows = tiled(a) ? kTiledRows : kRows, keys = tiled(a) ? kTiledKeys : kStepKeys;
   a.tiles = (int)(((int64_t)a.max_queries * a.group + rows - 1) / rows);
-  const int64_t blocks = (int64_t)a.n_seqs * a.tiles * a.n_kv_heads;
-  const int64_t most = (int64_t)a.pages_per_seq * a.page_size / kMinKeys;
-  const int64_t want = (tiled(a) ? 512 : 1024) / blocks;
-  a.splits = (int)(want < most ? (want > 1 ? want : 1) : (most > 1 ? most : 1));
   a.by_tiles = FastDiv(a.tiles);
-  a.by_splits = FastDiv(a.splits);
-  return a.splits == 1 ? 0 : (a.n_rows * a.splits * (a.head_dim + 2) * 4 + 255) / 256 * 256;
+  a.by_kv_heads = FastDiv(a.n_kv_heads);
+  a.planned = a.n_seqs <= kMaxPlanned;
+  a.shares_wanted = 0;
+  a.n_parts = 0;
+  int64_t tiles = (int64_t)a.n_seqs * a.tiles;
+  if (a.planned) tiles = std::min(tiles, (int64_t)a.n_tokens * a.group / rows + a.n_seqs);
+  a.units = (int)tiles;
+  const int64_t steps = ((int64_t)a.pages_per_seq * a.page_size + keys - 1) / keys;
+  const int64_t limit = slots(a) * (tiled(a) ? 1 : 2);
+  if (!a.planned || tiles * a.n_kv_heads >= limit || steps * keys <= kMinKeys ||
+      steps * tiles > 0x7FFFFFFF)
+    return 0;
+  // a sequence's last share is shorter than the others: half a share each
+  const int64_t want = std::max(tiles, (slots(a) - tiles * a.n_kv_heads / 2) / a.n_kv_heads);
+  const int64_t most = tiles * (steps * keys / kMinKeys + 1);  // units if all are of kMinKeys
+  a.shares_wanted = (int)want;
+  a.units = (int)std::min(tiles + want, most);
+  a.n_parts = (int64_t)a.units * a.n_kv_heads * rows;
+  return (a.n_parts * (a.head_dim + 2) * 4 + 255) / 256 * 256;
 }
 
 hipError_t mx_attention_launch(const AttentionArgs &a, hipStream_t stream) {
-  const int blocks = a.n_seqs * a.tiles * a.n_kv_heads;
+  const int blocks = a.units * a.n_kv_heads;
   hipError_t e;
   if (tiled(a)) {
-    e = attention_tiled_launch(a, blocks * a.splits, stream);
+    e = attention_tiled_launch(a, blocks, stream);
   } else {
     const int nd = (a.head_dim + 63) / 64;
-#define GO(NP, F, ND)                                                                         \
-  hipLaunchKernelGGL((attention_rows_kernel<NP, F, ND>), dim3(blocks * a.splits), dim3(256), 0, \
-                     stream, a)
+#define GO(NP, F, ND)                                                                            \
+  if (a.max_queries == 1)                                                                        \
+    hipLaunchKernelGGL((attention_rows_kernel<NP, F, ND, false>), dim3(blocks), dim3(256), 0,    \
+                       stream, a);                                                               \
+  else                                                                                           \
+    hipLaunchKernelGGL((attention_rows_kernel<NP, F, ND, true>), dim3(blocks), dim3(256), 0,     \
+                       stream, a)
 #define BY_DIM(NP, F)                    \
   switch (nd) {                          \
     case 1: GO(NP, F, 1); break;         \
@@ -434,13 +562,17 @@ hipError_t mx_attention_launch(const AttentionArgs &a, hipStream_t stream) {
 #undef GO
     e = hipGetLastError();
   }
-  if (e != hipSuccess || a.splits == 1) return e;
+  if (e != hipSuccess || a.n_parts == 0) return e;
+  const int64_t rows = (int64_t)a.max_queries * a.group;
+  const int64_t tiles = std::min((int64_t)a.n_seqs * a.tiles,
+                                 (int64_t)a.n_tokens * a.group / (tiled(a) ? kTiledRows : kRows) + a.n_seqs);
+  const int chunk = tiled(a) ? 16 : 4;
+  const dim3 grid((uint32_t)(tiles * a.n_kv_heads),
+                  (uint32_t)((std::min<int64_t>(rows, tiled(a) ? kTiledRows : kRows) + chunk - 1) / chunk));
   if (tiled(a))
-    hipLaunchKernelGGL((attention_join_kernel<kTiledRows, kTiledKeys>), dim3(blocks, kTiledRows / 16),
-                       dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((attention_join_kernel<kTiledRows, kTiledKeys>), grid, dim3(256), 0, stream, a);
   else
-    hipLaunchKernelGGL((attention_join_kernel<kRows, kStepKeys>), dim3(blocks), dim3(256), 0, stream,
-                       a);
+    hipLaunchKernelGGL((attention_join_kernel<kRows, kStepKeys>), grid, dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 

@@ -51,7 +51,7 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
   __shared__ __attribute__((aligned(16))) float powers[2][kTile];
   __shared__ __attribute__((aligned(16))) uint32_t staged[2][kWaves];
   Work w;
-  if (!work_of<kRows, kTile>(a, blockIdx.x, a.splits, w) || w.split >= w.splits) return;
+  if (!work_of<kRows, kTile>(a, blockIdx.x, w)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r32 = lane & 31, half = lane >> 5;
   const int D = a.head_dim, nb = D / 32;
@@ -70,11 +70,14 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
   {
     const int64_t at = (int64_t)(w.seq.q0 + token) * a.q_stride +
                        (int64_t)(w.kv_head * a.group + row - token * a.group) * D + 8 * half;
+    RawQ<NP> raw[DP / 16];
+#pragma unroll
+    for (int s = 0; s < DP / 16; s++) raw[s] = load_q8<NP>(a, at + (16 * s < D ? 16 * s : 0));
     float f[DP / 16][8];
     uint32_t amax = 0;
 #pragma unroll
     for (int s = 0; s < DP / 16; s++) {
-      if (16 * s < D) load_q8(a, at + 16 * s, f[s]);
+      q8_to_f32<NP>(a, raw[s], f[s]);
 #pragma unroll
       for (int i = 0; i < 8; i++) {
         if (16 * s >= D) f[s][i] = 0.0f;
@@ -102,7 +105,7 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
   const int32_t *const table = a.table + (int64_t)w.index * a.pages_per_seq;
   const int sub = lane & (LP - 1), lane_key = lane / LP;
   const bool has = 16 * sub < D;
-  const auto load = [&](int t, Data &d) {
+  const auto load = [&](int t, Data &d) __attribute__((always_inline)) {
 #pragma unroll
     for (int p = 0; p < PASSES; p++) {
       const int key = w.begin + t * kTile + kWaveKeys * wave + 64 / LP * p + lane_key;
@@ -129,13 +132,13 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
       }
     }
   };
-  const auto is_mixed = [&](int t) {
+  const auto is_mixed = [&](int t) __attribute__((always_inline)) {
     const int first = w.begin + t * kTile;
     return max(first, w.any.lo) < w.all.lo || min(first + kTile - 1, w.any.hi) > w.all.hi;
   };
 
   // The tile's share into LDS as fp16 (bf16 values where it is mixed).
-  const auto stage = [&](int t, const Data &d, int k_before, int v_before) {
+  const auto stage = [&](int t, const Data &d, int k_before, int v_before) __attribute__((always_inline)) {
     const int b = t & 1;
     const bool mixed = is_mixed(t);
     uint32_t top = 0;
@@ -195,13 +198,13 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
   const int k_at = r32 * KS + 16 * half;
 
   // 32 dims of the 16 keys of step n, transposed: keys 4 half .. + 3 and 8 + 4 half .. + 3
-  const auto value_operand = [&](int b, int n, int t) {
+  const auto value_operand = [&](int b, int n, int t) __attribute__((always_inline)) {
     const uint8_t *const at = v_lds[b] + v_at + 16 * n * VS + 64 * t;
     const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsS16x4 *)at);
     const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsS16x4 *)(at + 8 * VS));
     return s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
   };
-  const auto scores = [&](int b, f32x16 (&s)[2]) {
+  const auto scores = [&](int b, f32x16 (&s)[2]) __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < 2; j++) {
 #pragma unroll
@@ -215,7 +218,7 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
       }
     }
   };
-  const auto scale_sums = [&](float f, int v_new) {
+  const auto scale_sums = [&](float f, int v_new) __attribute__((always_inline)) {
     l *= f;
     const float o = __builtin_ldexpf(f, v_ref - v_new);
 #pragma unroll
@@ -223,7 +226,7 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
 #pragma unroll
       for (int i = 0; i < 16; i++) acc[t][i] *= o;
   };
-  const auto raise = [&](float mx, int v_new) {
+  const auto raise = [&](float mx, int v_new) __attribute__((always_inline)) {
     mx = swap_max32(mx);
     const float m_new = fmaxf(m, mx);
     if (__builtin_amdgcn_ballot_w64(m_new > m) != 0 || v_new != v_ref) {
@@ -233,7 +236,7 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
     return (m == kMinusInf ? 0.0f : m) - kWeightExponent;
   };
 
-  const auto compute = [&](int b, const Staged (&st)[kWaves], int v_new) {
+  const auto compute = [&](int b, const Staged (&st)[kWaves], int v_new) __attribute__((always_inline)) {
     f32x16 s[2];
     scores(b, s);
     float c[kWaves], mx = kMinusInf;
@@ -296,7 +299,7 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
     }
   };
 
-  const auto compute_mixed = [&](int b, int first, bool nans) {
+  const auto compute_mixed = [&](int b, int first, bool nans) __attribute__((always_inline)) {
     f32x16 s[2];
     scores(b, s);
     uint32_t sees = 0;
@@ -404,11 +407,9 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
   const int out_row = w.r0 + 32 * wave + r32;
   if (out_row > last_row) return;
   const int head = w.kv_head * a.group + row - token * a.group;
-  const int64_t flat = (int64_t)(w.seq.q0 + token) * a.n_kv_heads * a.group + head;
   const bool whole = w.splits == 1;
-  if (!whole && half == 0)
-    reinterpret_cast<float2 *>(a.partial + a.n_rows * a.splits * D)[flat * a.splits + w.split] =
-        make_float2(m, l);
+  const int64_t part = part_row<kRows>(a, w, w.split, 32 * wave + r32);
+  if (!whole && half == 0) part_stats(a)[part] = make_float2(m, l);
   const float inv = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
 #pragma unroll
   for (int t = 0; t < 2 * ND; t++)
@@ -420,7 +421,7 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
       for (int n = 0; n < 4; n++) v[n] = __builtin_ldexpf(acc[t][i + n] * inv, v_ref - X - 127);
       if (32 * t < D) {
         if (whole) store_y4(a, (int64_t)(w.seq.q0 + token) * a.y_stride + (int64_t)head * D + c, v);
-        else *reinterpret_cast<f32x4 *>(a.partial + (flat * a.splits + w.split) * D + c) = v;
+        else *reinterpret_cast<f32x4 *>(a.partial + part * D + c) = v;
       }
     }
 }

@@ -123,14 +123,17 @@ struct AttentionArgs {
   int64_t q_stride, y_stride;
   const int32_t *starts, *counts, *table;
   const uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
-  float *partial;  // [rows][splits][head_dim], then [rows][splits][2]
-  int64_t n_rows;  // n_tokens * n_heads
+  float *partial;   // [n_parts][head_dim], then [n_parts][2]
+  int64_t n_parts;  // rows of partial results
   int type, format, n_tokens, n_heads, n_kv_heads, group, head_dim;
   int n_seqs, pages_per_seq, max_queries, n_pages, page_size;
   int causal, window;  // window 0: none
-  int splits, tiles;   // ranges of keys; tiles of rows
+  // tiles of rows that a sequence has at most; where `planned`, workgroups find
+  // their sequence by its sizes, and cut the keys into shares for about
+  // shares_wanted (0: none) of them a key head; units they are at most
+  int tiles, planned, shares_wanted, units;
   float scale;         // times log2(e)
-  FastDiv by_page, by_group, by_kv_heads, by_tiles, by_splits;
+  FastDiv by_page, by_group, by_kv_heads, by_tiles;
 };
 // Sizes alone decide the launch: the same call has the same workspace.
 int64_t mx_attention_workspace_bytes(AttentionArgs &a);

@@ -194,7 +194,7 @@ bool valid_cache(int64_t n_tokens, int64_t n_heads, int64_t head_dim, int64_t n_
                  int64_t page_size) {
   return valid_count(n_tokens) && valid_heads(n_heads) && head_dim > 0 && head_dim % 32 == 0 &&
          head_dim <= 256 && page_size > 0 && page_size <= 65536 && valid_count(n_pages) &&
-         n_pages * page_size <= 0x7FFFFFFF;
+         n_pages <= 0x7FFFFFFF / (n_heads * page_size);
 }
 // Rows of `width` values with this many to the next, at most 2^31 of them.
 bool valid_stride(int64_t stride, int64_t width) { return stride >= width && stride <= 0x7FFFFFFF; }
@@ -230,7 +230,6 @@ bool attention_args(q4k::AttentionArgs &a, int64_t n_tokens, int64_t n_heads, in
   a.n_heads = (int)n_heads;
   a.n_kv_heads = (int)n_kv_heads;
   a.group = (int)(n_heads / n_kv_heads);
-  a.n_rows = n_tokens * n_heads;
   a.head_dim = (int)head_dim;
   a.n_seqs = (int)n_seqs;
   a.pages_per_seq = (int)pages_per_seq;
@@ -856,7 +855,6 @@ int mx_attention(const void *q, int64_t q_stride, int type, const int32_t *query
   a.scale = scale * 1.44269504088896340736f;
   a.by_page = q4k::FastDiv((uint32_t)page_size);
   a.by_group = q4k::FastDiv((uint32_t)a.group);
-  a.by_kv_heads = q4k::FastDiv((uint32_t)a.n_kv_heads);
   hipError_t e = q4k::mx_attention_launch(a, (hipStream_t)stream);
   return e == hipSuccess ? Q4K_OK : hip_fail(e, "mx_attention launch");
 }
