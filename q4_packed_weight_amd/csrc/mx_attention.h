@@ -241,14 +241,14 @@ __device__ __forceinline__ float block_scale(uint32_t s, int base) {
   return __builtin_bit_cast(float, s == 255 ? 0x7FC00000u : (uint32_t)e << 23);
 }
 
-// The values' reference, which what is summed up carries too: that of the keys
-// taken together, or the one before as long as it is no lower and at most 2^8
-// above, so that it seldom changes.  It may fall as well: a single large value
-// takes no bits from those of other keys.  Not below 64, or what was summed up
-// at 2^59 could leave fp32: values below 2^-55 lose bits.
-constexpr int kFirstValueRef = 127, kLastValueRef = 64;
-__device__ __forceinline__ int value_ref(int before, int top) {
-  const int now = max(top, kLastValueRef);
+// A reference: that of the keys taken together, or the one before as long as it
+// is no lower and at most 2^8 above, so that it seldom changes.  What is summed up
+// carries the values'.  It may fall as well: a single large value takes no bits
+// from those of other keys.  Not below 64, or what was summed up at 2^59 could
+// leave fp32: keys and values below 2^-55 lose bits.
+constexpr int kFirstRef = 127, kLastRef = 64;
+__device__ __forceinline__ int reference(int before, int top) {
+  const int now = max(top, kLastRef);
   return now > before || now + 8 < before ? now : before;
 }
 

@@ -166,7 +166,7 @@ __global__ __launch_bounds__(kWaves * 64, MIXED ? 1 : (kWavesPerSimd<NP, ND>)) v
 #pragma unroll
   for (int i = 0; i < 4 * ND; i++) acc[i] = f32x4{0, 0, 0, 0};
   float m = kMinusInf, l = 0.0f;
-  int v_ref = kFirstValueRef;
+  int v_ref = kFirstRef;
   uint8_t *const mem = lds + wave * kRegion;
   typedef __attribute__((address_space(3))) s16x4 LdsS16x4;
   const uint8_t *const read_at = mem + (4 * g + (r16 >> 2)) * VS + 8 * (r16 & 3);
@@ -220,7 +220,7 @@ __global__ __launch_bounds__(kWaves * 64, MIXED ? 1 : (kWavesPerSimd<NP, ND>)) v
   // Keys that all rows see (or none: absent ones).  The references stay as long
   // as no scale of the step is above them and one at least is no more than 2^8
   // below, which each lane compares for itself; else they are made anew.
-  int k_ref = kFirstValueRef;
+  int k_ref = kFirstRef;
   const auto compute = [&](int step) __attribute__((always_inline)) {
     uint32_t k_top = 0, v_top = 0;
 #pragma unroll
@@ -235,8 +235,8 @@ __global__ __launch_bounds__(kWaves * 64, MIXED ? 1 : (kWavesPerSimd<NP, ND>)) v
     int v_new = v_ref;
     bool nans = false;
     if (__builtin_amdgcn_ballot_w64((int)k_top > k_ref || (int)v_top > v_ref) != 0 ||
-        __builtin_amdgcn_ballot_w64((int)k_top + 8 >= k_ref) == 0 ||
-        __builtin_amdgcn_ballot_w64((int)v_top + 8 >= v_ref) == 0) {
+        (k_ref != kLastRef && __builtin_amdgcn_ballot_w64((int)k_top + 8 >= k_ref) == 0) ||
+        (v_ref != kLastRef && __builtin_amdgcn_ballot_w64((int)v_top + 8 >= v_ref) == 0)) {
       nans = __builtin_amdgcn_ballot_w64(max(k_top, v_top) == 255) != 0;
       uint32_t top = 0;
 #pragma unroll
@@ -245,8 +245,8 @@ __global__ __launch_bounds__(kWaves * 64, MIXED ? 1 : (kWavesPerSimd<NP, ND>)) v
         for (int p = 0; p < ND; p++)
           top = pk_max(top, scale_rank(d.ks[j].of(p)) | scale_rank(d.vs[j].of(p)) << 16);
       top = wave_pk_max(top);
-      k_ref = value_ref(k_ref, (int)(top & 0xFFFF));
-      v_new = value_ref(v_ref, (int)(top >> 16));
+      k_ref = reference(k_ref, (int)(top & 0xFFFF));
+      v_new = reference(v_ref, (int)(top >> 16));
     }
     float kf[2][ND], vf[2][ND];
 #pragma unroll

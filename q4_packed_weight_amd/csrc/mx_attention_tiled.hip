@@ -12,14 +12,9 @@ static_assert(kRows == 32 * kWaves, "32 rows a wave");
 constexpr int kWaveKeys = kTile / kWaves;  // that a wave stages: 16, one step of V^T P^T
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-// What a wave says of the 16 keys it has staged.
-struct Staged {
-  uint32_t word;
-  __device__ __forceinline__ int k_ref() const { return word & 255; }
-  __device__ __forceinline__ int v_ref() const { return word >> 8 & 255; }
-  __device__ __forceinline__ bool missing() const { return word >> 16 & 1; }
-  __device__ __forceinline__ bool nans() const { return word >> 17 & 1; }
-};
+// What a wave says of the 16 keys it has staged: a scale above its reference,
+// one at most 2^8 below it, a page that is none, a NaN value (mixed tiles).
+enum : uint32_t { kOver = 1, kNearK = 2, kNearV = 4, kAbsent = 8, kNan = 16 };
 
 // A wave's share of a tile as it lies in memory: 16 codes (dims 16 n .. of lane
 // n of a key's LP lanes) in each pass.
@@ -27,8 +22,9 @@ template <int FMT, int ND> struct TileData {
   static constexpr int LP = ND == 1 ? 4 : ND == 2 ? 8 : 16;
   static constexpr int PASSES = kWaveKeys * LP / 64;
   static constexpr int W = FMT == MX_FP8 ? 4 : 2;
-  uint32_t k[PASSES][W], v[PASSES][W], ks[PASSES], vs[PASSES];
-  bool ok[PASSES];
+  uint32_t k[PASSES][W], v[PASSES][W];
+  uint8_t ks[PASSES], vs[PASSES];
+  bool ok[PASSES];  // a key that some row sees, in a page that there is
 };
 
 template <int LP> __device__ __forceinline__ uint32_t max_of_key(uint32_t v) {
@@ -49,7 +45,7 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
   __shared__ __attribute__((aligned(16))) uint8_t k_lds[2][kTile * KS];
   __shared__ __attribute__((aligned(16))) uint8_t v_lds[2][kTile * VS];
   __shared__ __attribute__((aligned(16))) float powers[2][kTile];
-  __shared__ __attribute__((aligned(16))) uint32_t staged[2][kWaves];
+  __shared__ __attribute__((aligned(16))) uint32_t staged[2][kWaves], tops[kWaves];
   Work w;
   if (!work_of<kRows, kTile>(a, blockIdx.x, w)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -105,52 +101,60 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
   const int32_t *const table = a.table + (int64_t)w.index * a.pages_per_seq;
   const int sub = lane & (LP - 1), lane_key = lane / LP;
   const bool has = 16 * sub < D;
-  const auto load = [&](int t, Data &d) __attribute__((always_inline)) {
+  // Pages of the keys, then their codes: every lane loads, absent keys row 0 of
+  // their head, lanes behind head_dim dims 0, without a branch; stage puts zeros there.
+  Data d;
+  int pages[PASSES];
+  const auto load_pages = [&](int t) __attribute__((always_inline)) {
 #pragma unroll
     for (int p = 0; p < PASSES; p++) {
       const int key = w.begin + t * kTile + kWaveKeys * wave + 64 / LP * p + lane_key;
-      bool ok = t < w.last && key >= w.any.lo && key <= w.any.hi;
-      int page = 0, at = 0;
-      if (ok) {
-        at = a.by_page.of(key);
-        page = table[at];
-        ok = page >= 0 && page < a.n_pages;
-      }
-      const int64_t r = ((int64_t)page * a.n_kv_heads + w.kv_head) * a.page_size +
-                        (key - at * a.page_size);
-      d.ok[p] = ok;
-      d.ks[p] = d.vs[p] = 0;
-#pragma unroll
-      for (int i = 0; i < W; i++) d.k[p][i] = d.v[p][i] = 0;
-      if (ok && has) {
-        const int64_t c = r * code_row + 16 * sub * (FMT == MX_FP8 ? 2 : 1) / 2;
-        const int64_t s = r * nb + (sub >> 1);
-        load_codes(a.k_codes + c, d.k[p]);
-        load_codes(a.v_codes + c, d.v[p]);
-        d.ks[p] = a.k_scales[s];
-        d.vs[p] = a.v_scales[s];
-      }
+      pages[p] = table[a.by_page.of(min(max(key, w.any.lo), w.any.hi))];
     }
   };
-  const auto is_mixed = [&](int t) __attribute__((always_inline)) {
-    const int first = w.begin + t * kTile;
-    return max(first, w.any.lo) < w.all.lo || min(first + kTile - 1, w.any.hi) > w.all.hi;
-  };
-
-  // The tile's share into LDS as fp16 (bf16 values where it is mixed).
-  const auto stage = [&](int t, const Data &d, int k_before, int v_before) __attribute__((always_inline)) {
-    const int b = t & 1;
-    const bool mixed = is_mixed(t);
-    uint32_t top = 0;
-    bool missing = false, nan = false;
+  const auto load = [&](int t) __attribute__((always_inline)) {
 #pragma unroll
     for (int p = 0; p < PASSES; p++) {
-      top = pk_max(top, scale_rank(d.ks[p]) | scale_rank(d.vs[p]) << 16);
-      missing |= !d.ok[p];
+      const int key = w.begin + t * kTile + kWaveKeys * wave + 64 / LP * p + lane_key;
+      d.ok[p] = key >= w.any.lo && key <= w.any.hi && (uint32_t)pages[p] < (uint32_t)a.n_pages;
+      const uint32_t place = key - a.by_page.of(key) * a.page_size;
+      const uint32_t r = d.ok[p] ? (pages[p] * a.n_kv_heads + w.kv_head) * a.page_size + place : 0;
+      const uint64_t c = (uint64_t)r * code_row + (has ? 16 * sub * (FMT == MX_FP8 ? 2 : 1) / 2 : 0);
+      const uint64_t s = (uint64_t)r * nb + (has ? sub >> 1 : 0);
+      load_codes(a.k_codes + c, d.k[p]);
+      load_codes(a.v_codes + c, d.v[p]);
+      d.ks[p] = a.k_scales[s];
+      d.vs[p] = a.v_scales[s];
     }
-    top = wave_pk_max(top);
-    missing = __builtin_amdgcn_ballot_w64(missing) != 0;
-    const int k_ref = value_ref(k_before, top & 0xFFFF), v_ref = value_ref(v_before, top >> 16);
+  };
+  // keys that some rows see and others do not, or none
+  const auto is_mixed = [&](int t) __attribute__((always_inline)) {
+    const int first = w.begin + t * kTile;
+    return first < w.all.lo || first + kTile - 1 > w.all.hi;
+  };
+  int k_ref = kFirstRef, v_ref = kFirstRef;
+  const bool odd = DP != D || LP * 16 != DP;
+
+  // The tile's share into LDS as fp16 under the references (mixed: keys under
+  // their own, values as bf16).
+  const auto stage = [&](int t, bool mixed) __attribute__((always_inline)) {
+    const int b = t & 1;
+    bool absent = false, nan = false;
+    uint32_t k_top = 0, v_top = 0;
+#pragma unroll
+    for (int p = 0; p < PASSES; p++) absent |= !d.ok[p];
+    absent = __builtin_amdgcn_ballot_w64(absent) != 0;
+    if (absent || odd) {
+#pragma unroll
+      for (int p = 0; p < PASSES; p++) {
+        if (!d.ok[p] || !has) {
+#pragma unroll
+          for (int i = 0; i < W; i++) d.k[p][i] = d.v[p][i] = 0;
+          d.ks[p] = d.vs[p] = 0;
+        }
+      }
+    }
+    const bool writes = LP * 16 == DP || 16 * sub < DP;
 #pragma unroll
     for (int p = 0; p < PASSES; p++) {
       const int n = kWaveKeys * wave + 64 / LP * p + lane_key;
@@ -161,29 +165,36 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
         k_base = 127 + X - own;
         nan |= has_nan<FMT>(d.v[p], d.vs[p]);
         if (sub == 0) powers[b][n] = d.ok[p] ? __builtin_ldexpf(1.0f, own - X - 127) : -1.0f;
-        if (LP * 16 == DP || 16 * sub < DP) {
+        if (writes) {
           const float s = block_scale(d.vs[p], 0);
           *reinterpret_cast<bf16x8 *>(v_to) = codes_operand_bf16<FMT>(&d.v[p][0], s);
           *reinterpret_cast<bf16x8 *>(v_to + 16) = codes_operand_bf16<FMT>(&d.v[p][W / 2], s);
         }
       } else {
-        if (missing && sub == 0) powers[b][n] = d.ok[p] ? 1.0f : -1.0f;
-        if (LP * 16 == DP || 16 * sub < DP) {
+        k_top = max(k_top, scale_rank(d.ks[p]));
+        v_top = max(v_top, scale_rank(d.vs[p]));
+        if (writes) {
           const float s = block_scale(d.vs[p], 127 + X - v_ref);
           *reinterpret_cast<half8_t *>(v_to) = codes_operand<FMT>(&d.v[p][0], s);
           *reinterpret_cast<half8_t *>(v_to + 16) = codes_operand<FMT>(&d.v[p][W / 2], s);
         }
       }
-      if (LP * 16 == DP || 16 * sub < DP) {
+      if (writes) {
         const float s = block_scale(d.ks[p], k_base);
         *reinterpret_cast<half8_t *>(k_to) = codes_operand<FMT>(&d.k[p][0], s);
         *reinterpret_cast<half8_t *>(k_to + 16) = codes_operand<FMT>(&d.k[p][W / 2], s);
       }
     }
-    if (mixed) nan = __builtin_amdgcn_ballot_w64(nan) != 0;
-    if (lane == 0)
-      staged[b][wave] = (uint32_t)k_ref | (uint32_t)v_ref << 8 | (missing ? 1u << 16 : 0) |
-                        (nan ? 1u << 17 : 0);
+    uint32_t word = 0;
+    if (mixed) {
+      if (__builtin_amdgcn_ballot_w64(nan) != 0) word = kNan;
+    } else {
+      if (__builtin_amdgcn_ballot_w64((int)k_top > k_ref || (int)v_top > v_ref) != 0) word |= kOver;
+      if (k_ref == kLastRef || __builtin_amdgcn_ballot_w64((int)k_top + 8 >= k_ref) != 0) word |= kNearK;
+      if (v_ref == kLastRef || __builtin_amdgcn_ballot_w64((int)v_top + 8 >= v_ref) != 0) word |= kNearV;
+      if (absent) word |= kAbsent;
+    }
+    if (lane == 0) staged[b][wave] = word;
   };
 
   f32x16 acc[2 * ND];
@@ -192,7 +203,6 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
 #pragma unroll
     for (int i = 0; i < 16; i++) acc[t][i] = 0.0f;
   float m = kMinusInf, l = 0.0f;
-  int k_ref = kFirstValueRef, v_ref = kFirstValueRef;
   typedef __attribute__((address_space(3))) s16x4 LdsS16x4;
   const int v_at = (4 * half + (lane >> 2 & 3)) * VS + 32 * (lane >> 4 & 1) + 8 * (lane & 3);
   const int k_at = r32 * KS + 16 * half;
@@ -226,68 +236,34 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
 #pragma unroll
       for (int i = 0; i < 16; i++) acc[t][i] *= o;
   };
-  const auto raise = [&](float mx, int v_new) __attribute__((always_inline)) {
+  // as in the form for few rows: a maximum up to 2^4 too low stays
+  const auto raise = [&](float mx) __attribute__((always_inline)) {
     mx = swap_max32(mx);
-    const float m_new = fmaxf(m, mx);
-    if (__builtin_amdgcn_ballot_w64(m_new > m) != 0 || v_new != v_ref) {
-      scale_sums(m_new > m ? __builtin_amdgcn_exp2f(m - m_new) : 1.0f, v_new);
-      m = m_new;
+    const bool up = mx > m + 4.0f;
+    if (__builtin_amdgcn_ballot_w64(up) != 0) {
+      scale_sums(up ? __builtin_amdgcn_exp2f(m - mx) : 1.0f, v_ref);
+      m = up ? mx : m;
     }
     return (m == kMinusInf ? 0.0f : m) - kWeightExponent;
   };
 
-  const auto compute = [&](int b, const Staged (&st)[kWaves], int v_new) __attribute__((always_inline)) {
+  const auto compute = [&](int b) __attribute__((always_inline)) {
     f32x16 s[2];
     scores(b, s);
-    float c[kWaves], mx = kMinusInf;
+    const float c = __builtin_ldexpf(row_scale, k_ref - X - 127);
+    float mx = s[0][0];
 #pragma unroll
-    for (int n = 0; n < kWaves; n++) {
-      c[n] = __builtin_ldexpf(row_scale, st[n].k_ref() - X - 127);
-      float top;
-      if (st[n].missing()) {
-        top = kMinusInf;
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-          const float x = s[n >> 1][8 * (n & 1) + i];
-          const bool gone = powers[b][16 * n + 8 * (i >> 2) + 4 * half + (i & 3)] < 0.0f;
-          s[n >> 1][8 * (n & 1) + i] = gone ? kMinusInf : x;
-          top = gone ? top : fmaxf(top, x);
-        }
-        if (top != kMinusInf) top *= c[n];
-      } else {
-        top = s[n >> 1][8 * (n & 1)];
-#pragma unroll
-        for (int i = 1; i < 8; i++) top = fmaxf(top, s[n >> 1][8 * (n & 1) + i]);
-        top *= c[n];
-      }
-      mx = fmaxf(mx, top);
-    }
-    const float less = raise(mx, v_new);
+    for (int i = 1; i < 32; i++) mx = fmaxf(mx, s[i >> 4][i & 15]);
+    const float less = raise(mx * c);
 #pragma unroll
     for (int n = 0; n < kWaves; n++) {
       half8_t p[NP];
-      float e[8];
 #pragma unroll
       for (int i = 0; i < 8; i++) {
-        const float x = s[n >> 1][8 * (n & 1) + i];
-        e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x, c[n], -less));
-      }
-      if (st[n].missing()) {  // not -inf * c, where c is 0 or NaN
-#pragma unroll
-        for (int i = 0; i < 8; i++) e[i] = s[n >> 1][8 * (n & 1) + i] == kMinusInf ? 0.0f : e[i];
-      }
-#pragma unroll
-      for (int i = 0; i < 8; i++) l += e[i];
-      const int lower = v_new - st[n].v_ref();
-      if (lower != 0) {
-        const float f = __builtin_ldexpf(1.0f, -lower);
-#pragma unroll
-        for (int i = 0; i < 8; i++) e[i] *= f;
-      }
-#pragma unroll
-      for (int i = 0; i < 8; i++) {
-        p[0][i] = (_Float16)e[i];
-        if constexpr (NP == 2) p[1][i] = (_Float16)(e[i] - (float)p[0][i]);
+        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n >> 1][8 * (n & 1) + i], c, -less));
+        l += e;
+        p[0][i] = (_Float16)e;
+        if constexpr (NP == 2) p[1][i] = (_Float16)(e - (float)p[0][i]);
       }
 #pragma unroll
       for (int t = 0; t < 2 * ND; t++) {
@@ -319,7 +295,7 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
           mx = fmaxf(mx, s[j][i + n]);
         }
       }
-    const float less = raise(mx, v_ref);
+    const float less = raise(mx);
     const float f = __builtin_ldexpf(1.0f, 127 + X - v_ref);  // values are not scaled here
 #pragma unroll
     for (int n = 0; n < kWaves; n++) {
@@ -367,38 +343,67 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
     }
   };
 
-  Data d;
-  load(w.first, d);
-  if (w.first < w.last) stage(w.first, d, k_ref, v_ref);
-  load(w.first + 1, d);
+  // a tile again, under references that are right for it or, where a page is none,
+  // as a mixed one; seldom more than once
+  const auto stage_again = [&](int t, bool absent) __attribute__((always_inline)) {
+    load_pages(t);
+    load(t);
+    uint32_t top = 0;
+#pragma unroll
+    for (int p = 0; p < PASSES; p++)
+      top = pk_max(top, d.ok[p] && has ? scale_rank(d.ks[p]) | scale_rank(d.vs[p]) << 16 : 0);
+    top = wave_pk_max(top);
+    if (lane == 0) tops[wave] = top;
+    __syncthreads();
+    if (!absent) {
+      top = pk_max(pk_max(tops[0], tops[1]), pk_max(tops[2], tops[3]));
+      top = (uint32_t)__builtin_amdgcn_readfirstlane((int)top);
+      k_ref = reference(k_ref, top & 0xFFFF);
+      const int v_new = reference(v_ref, top >> 16);
+      scale_sums(1.0f, v_new);
+      v_ref = v_new;
+    }
+    stage(t, absent);
+    __syncthreads();
+    load_pages(t + 1);
+    load(t + 1);
+    load_pages(t + 2);
+  };
+
+  if (w.first < w.last) {
+    load_pages(w.first);
+    load(w.first);
+    load_pages(w.first + 1);
+    stage(w.first, is_mixed(w.first));
+    load(w.first + 1);
+    load_pages(w.first + 2);
+  }
   __syncthreads();
   for (int t = w.first; t < w.last; t++) {
     const int b = t & 1, first = w.begin + t * kTile;
-    const bool mixed = is_mixed(t);
-    Staged st[kWaves];
+    bool mixed = is_mixed(t);
+    uint32_t any;
     {
       const u32x4 words = *reinterpret_cast<const u32x4 *>(&staged[b][0]);
-#pragma unroll
-      for (int n = 0; n < kWaves; n++)
-        st[n].word = (uint32_t)__builtin_amdgcn_readfirstlane((int)words[n]);
+      any = (uint32_t)__builtin_amdgcn_readfirstlane((int)(words[0] | words[1] | words[2] | words[3]));
     }
-    int k_new = k_ref, v_new = v_ref;
-    if (!mixed) {
-      k_new = max(max(st[0].k_ref(), st[1].k_ref()), max(st[2].k_ref(), st[3].k_ref()));
-      v_new = value_ref(v_ref, max(max(st[0].v_ref(), st[1].v_ref()), max(st[2].v_ref(), st[3].v_ref())));
+    if (!mixed && (any & (kOver | kNearK | kNearV | kAbsent)) != (kNearK | kNearV)) {
+      mixed = (any & kAbsent) != 0;
+      stage_again(t, mixed);
+      if (mixed) {
+        const u32x4 words = *reinterpret_cast<const u32x4 *>(&staged[b][0]);
+        any = (uint32_t)__builtin_amdgcn_readfirstlane((int)(words[0] | words[1] | words[2] | words[3]));
+      }
     }
     if (t + 1 < w.last) {
-      stage(t + 1, d, k_new, v_new);
-      load(t + 2, d);
+      stage(t + 1, is_mixed(t + 1));
+      if (t + 2 < w.last) load(t + 2);
+      load_pages(t + 3);
     }
     if (active && max(first, one.lo) <= min(first + kTile - 1, two.hi)) {
-      if (mixed) compute_mixed(b, first, (st[0].word | st[1].word | st[2].word | st[3].word) >> 17 & 1);
-      else compute(b, st, v_new);
-    } else if (v_new != v_ref) {
-      scale_sums(1.0f, v_new);
+      if (mixed) compute_mixed(b, first, (any & kNan) != 0);
+      else compute(b);
     }
-    k_ref = k_new;
-    v_ref = v_new;
     __syncthreads();
   }
 
