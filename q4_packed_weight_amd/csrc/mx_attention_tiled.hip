@@ -35,7 +35,9 @@ template <int LP> __device__ __forceinline__ uint32_t max_of_key(uint32_t v) {
   return v;
 }
 
-template <int NP, int FMT, int ND>
+// WHOLE: pages of a multiple of 16 keys, so that a wave's 16 lie in one and
+// their addresses are scalars.
+template <int NP, int FMT, int ND, bool WHOLE>
 __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_kernel(AttentionArgs a) {
   constexpr int DP = 64 * ND;
   constexpr int KS = 2 * DP + 16, VS = 2 * DP + 32;  // bytes of a key's row in LDS
@@ -99,32 +101,41 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
   }
 
   const int32_t *const table = a.table + (int64_t)w.index * a.pages_per_seq;
-  const int sub = lane & (LP - 1), lane_key = lane / LP;
+  const int sub = lane & (LP - 1), lane_key = lane / LP;  // of a wave's pass
   const bool has = 16 * sub < D;
-  // Pages of the keys, then their codes: every lane loads, absent keys row 0 of
-  // their head, lanes behind head_dim dims 0, without a branch; stage puts zeros there.
+  // Pages of the keys, then their codes: every lane loads, absent keys a row that
+  // there is, lanes behind head_dim dims 0, without a branch; stage puts zeros there.
   Data d;
-  int pages[PASSES];
+  int pages[WHOLE ? 1 : PASSES];
+  const auto key_of = [&](int t, int p) __attribute__((always_inline)) {
+    return w.begin + t * kTile + kWaveKeys * wave + (WHOLE ? 0 : 64 / LP * p + lane_key);
+  };
   const auto load_pages = [&](int t) __attribute__((always_inline)) {
 #pragma unroll
-    for (int p = 0; p < PASSES; p++) {
-      const int key = w.begin + t * kTile + kWaveKeys * wave + 64 / LP * p + lane_key;
-      pages[p] = table[a.by_page.of(min(max(key, w.any.lo), w.any.hi))];
-    }
+    for (int p = 0; p < (WHOLE ? 1 : PASSES); p++)
+      pages[p] = table[a.by_page.of(min(max(key_of(t, p), w.any.lo), w.any.hi))];
   };
+  const uint32_t lane_code = (WHOLE ? lane_key * (int)code_row : 0) +
+                             (has ? 16 * sub * (FMT == MX_FP8 ? 2 : 1) / 2 : 0);
+  const uint32_t lane_scale = (WHOLE ? lane_key * nb : 0) + (has ? sub >> 1 : 0);
   const auto load = [&](int t) __attribute__((always_inline)) {
+    const uint8_t *k, *v, *ks, *vs;
 #pragma unroll
     for (int p = 0; p < PASSES; p++) {
-      const int key = w.begin + t * kTile + kWaveKeys * wave + 64 / LP * p + lane_key;
-      d.ok[p] = key >= w.any.lo && key <= w.any.hi && (uint32_t)pages[p] < (uint32_t)a.n_pages;
-      const uint32_t place = key - a.by_page.of(key) * a.page_size;
-      const uint32_t r = d.ok[p] ? (pages[p] * a.n_kv_heads + w.kv_head) * a.page_size + place : 0;
-      const uint64_t c = (uint64_t)r * code_row + (has ? 16 * sub * (FMT == MX_FP8 ? 2 : 1) / 2 : 0);
-      const uint64_t s = (uint64_t)r * nb + (has ? sub >> 1 : 0);
-      load_codes(a.k_codes + c, d.k[p]);
-      load_codes(a.v_codes + c, d.v[p]);
-      d.ks[p] = a.k_scales[s];
-      d.vs[p] = a.v_scales[s];
+      if (!WHOLE || p == 0) {
+        const int key = key_of(t, p);
+        d.ok[p] = (uint32_t)pages[p] < (uint32_t)a.n_pages && (WHOLE || (key >= w.any.lo && key <= w.any.hi));
+        const uint32_t place = key - a.by_page.of(key) * a.page_size;
+        const uint32_t r = d.ok[p] ? (pages[p] * a.n_kv_heads + w.kv_head) * a.page_size + place : 0;
+        const uint64_t c = (uint64_t)r * code_row, s = (uint64_t)r * nb;
+        k = a.k_codes + c, v = a.v_codes + c, ks = a.k_scales + s, vs = a.v_scales + s;
+      }
+      const uint32_t c = lane_code + (WHOLE ? 64 / LP * p * (int)code_row : 0);
+      const uint32_t s = lane_scale + (WHOLE ? 64 / LP * p * nb : 0);
+      load_codes(k + c, d.k[p]);
+      load_codes(v + c, d.v[p]);
+      d.ks[p] = ks[s];
+      d.vs[p] = vs[s];
     }
   };
   // keys that some rows see and others do not, or none
@@ -141,8 +152,22 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
     const int b = t & 1;
     bool absent = false, nan = false;
     uint32_t k_top = 0, v_top = 0;
+    if constexpr (WHOLE) {
+      absent = !d.ok[0];
 #pragma unroll
-    for (int p = 0; p < PASSES; p++) absent |= !d.ok[p];
+      for (int p = 1; p < PASSES; p++) d.ok[p] = d.ok[0];
+      if (mixed) {
+#pragma unroll
+        for (int p = 0; p < PASSES; p++) {
+          const int key = key_of(t, 0) + 64 / LP * p + lane_key;
+          d.ok[p] = d.ok[p] && key >= w.any.lo && key <= w.any.hi;
+          absent |= !d.ok[p];
+        }
+      }
+    } else {
+#pragma unroll
+      for (int p = 0; p < PASSES; p++) absent |= !d.ok[p];
+    }
     absent = __builtin_amdgcn_ballot_w64(absent) != 0;
     if (absent || odd) {
 #pragma unroll
@@ -351,7 +376,7 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
     uint32_t top = 0;
 #pragma unroll
     for (int p = 0; p < PASSES; p++)
-      top = pk_max(top, d.ok[p] && has ? scale_rank(d.ks[p]) | scale_rank(d.vs[p]) << 16 : 0);
+      top = pk_max(top, d.ok[WHOLE ? 0 : p] && has ? scale_rank(d.ks[p]) | scale_rank(d.vs[p]) << 16 : 0);
     top = wave_pk_max(top);
     if (lane == 0) tops[wave] = top;
     __syncthreads();
@@ -435,9 +460,13 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
 
 hipError_t attention_tiled_launch(const AttentionArgs &a, int blocks, hipStream_t stream) {
   const int nd = (a.head_dim + 63) / 64;
-#define GO(NP, F, ND)                                                                     \
-  hipLaunchKernelGGL((attention_tiled_kernel<NP, F, ND>), dim3(blocks), dim3(kWaves * 64), 0, \
-                     stream, a)
+#define GO(NP, F, ND)                                                                          \
+  if (a.page_size % kWaveKeys == 0)                                                            \
+    hipLaunchKernelGGL((attention_tiled_kernel<NP, F, ND, true>), dim3(blocks),                \
+                       dim3(kWaves * 64), 0, stream, a);                                       \
+  else                                                                                         \
+    hipLaunchKernelGGL((attention_tiled_kernel<NP, F, ND, false>), dim3(blocks),               \
+                       dim3(kWaves * 64), 0, stream, a)
 #define BY_DIM(NP, F)                    \
   switch (nd) {                          \
     case 1: GO(NP, F, 1); break;         \
