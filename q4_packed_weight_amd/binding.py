@@ -518,9 +518,12 @@ def _rows(t, dtype, name, rows, heads, head_dim):
     """(pointer, values from a row to the next) of [rows][heads * head_dim] or
     [rows][heads][head_dim] values; rows may lie apart, as slices of a wider
     matrix do."""
-    if t is None:
-        return None, heads * head_dim
     width = heads * head_dim
+    if t is None:
+        return None, width
+    if (t.dtype is dtype and t.is_cuda and t.numel() == rows * width and t.is_contiguous()
+            and t.shape[0] == rows and t.get_device() == _current_device()):
+        return t.data_ptr(), width
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:

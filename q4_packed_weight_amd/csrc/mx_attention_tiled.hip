@@ -1,5 +1,7 @@
 // mx_attention_tiled.hip -- attention over a paged MX cache for many rows:
 // chunks of new tokens, 32 rows a wave.
+#include <type_traits>
+
 #include "mx_attention.h"
 
 namespace q4k {
@@ -27,6 +29,12 @@ template <int FMT, int ND> struct TileData {
   bool ok[PASSES];  // a key that some row sees, in a page that there is
 };
 
+// A copy that the compiler does not see through.
+__device__ __forceinline__ int in_place(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 template <int LP> __device__ __forceinline__ uint32_t max_of_key(uint32_t v) {
   v = max_dpp_step<0xB1>(v);
   v = max_dpp_step<0x4E>(v);
@@ -40,7 +48,7 @@ template <int LP> __device__ __forceinline__ uint32_t max_of_key(uint32_t v) {
 template <int NP, int FMT, int ND, bool WHOLE>
 __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_kernel(AttentionArgs a) {
   constexpr int DP = 64 * ND;
-  constexpr int KS = 2 * DP + 16, VS = 2 * DP + 32;  // bytes of a key's row in LDS
+  constexpr int KS = 2 * DP + 16, VS = 2 * DP + 64;  // bytes of a key's row in LDS, over all banks
   constexpr int X = kCodeExponent<FMT>;
   typedef TileData<FMT, ND> Data;
   constexpr int LP = Data::LP, PASSES = Data::PASSES, W = Data::W;
@@ -101,32 +109,42 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
   }
 
   const int32_t *const table = a.table + (int64_t)w.index * a.pages_per_seq;
-  const int sub = lane & (LP - 1), lane_key = lane / LP;  // of a wave's pass
-  const bool has = 16 * sub < D;
+  // Key of a wave's pass and 16 dims of it; lanes behind head_dim do what the
+  // key's first lane does, and the keys' columns there are zeros once and for all.
+  const int lane_key = lane / LP, sub = 16 * (lane & (LP - 1)) < D ? lane & (LP - 1) : 0;
+  if (D != DP) {
+    const int pad = (DP - D) / 8;
+    for (int i = threadIdx.x; i < 2 * kTile * pad; i += kWaves * 64)
+      *reinterpret_cast<u32x4 *>(k_lds[0] + i / pad * KS + 2 * D + 16 * (i % pad)) = u32x4{0, 0, 0, 0};
+  }
   // Pages of the keys, then their codes: every lane loads, absent keys a row that
-  // there is, lanes behind head_dim dims 0, without a branch; stage puts zeros there.
+  // there is, without a branch; stage puts zeros there.
   Data d;
   int pages[WHOLE ? 1 : PASSES];
   const auto key_of = [&](int t, int p) __attribute__((always_inline)) {
     return w.begin + t * kTile + kWaveKeys * wave + (WHOLE ? 0 : 64 / LP * p + lane_key);
   };
+  // The compiler must not know that one page is the same for all lanes, or it waits
+  // for it, and so for all loads before it, at once, to have it in a scalar.
+  const int of_lane = in_place(0);
   const auto load_pages = [&](int t) __attribute__((always_inline)) {
 #pragma unroll
     for (int p = 0; p < (WHOLE ? 1 : PASSES); p++)
-      pages[p] = table[a.by_page.of(min(max(key_of(t, p), w.any.lo), w.any.hi))];
+      pages[p] = table[a.by_page.of(min(max(key_of(t, p), w.any.lo), w.any.hi)) + (WHOLE ? of_lane : 0)];
   };
   const uint32_t lane_code = (WHOLE ? lane_key * (int)code_row : 0) +
-                             (has ? 16 * sub * (FMT == MX_FP8 ? 2 : 1) / 2 : 0);
-  const uint32_t lane_scale = (WHOLE ? lane_key * nb : 0) + (has ? sub >> 1 : 0);
+                             16 * sub * (FMT == MX_FP8 ? 2 : 1) / 2;
+  const uint32_t lane_scale = (WHOLE ? lane_key * nb : 0) + (sub >> 1);
   const auto load = [&](int t) __attribute__((always_inline)) {
     const uint8_t *k, *v, *ks, *vs;
 #pragma unroll
     for (int p = 0; p < PASSES; p++) {
       if (!WHOLE || p == 0) {
         const int key = key_of(t, p);
-        d.ok[p] = (uint32_t)pages[p] < (uint32_t)a.n_pages && (WHOLE || (key >= w.any.lo && key <= w.any.hi));
+        const int page = WHOLE ? __builtin_amdgcn_readfirstlane(pages[p]) : pages[p];
+        d.ok[p] = t < w.last && (uint32_t)page < (uint32_t)a.n_pages && (WHOLE || (key >= w.any.lo && key <= w.any.hi));
         const uint32_t place = key - a.by_page.of(key) * a.page_size;
-        const uint32_t r = d.ok[p] ? (pages[p] * a.n_kv_heads + w.kv_head) * a.page_size + place : 0;
+        const uint32_t r = d.ok[p] ? (page * a.n_kv_heads + w.kv_head) * a.page_size + place : 0;
         const uint64_t c = (uint64_t)r * code_row, s = (uint64_t)r * nb;
         k = a.k_codes + c, v = a.v_codes + c, ks = a.k_scales + s, vs = a.v_scales + s;
       }
@@ -144,7 +162,6 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
     return first < w.all.lo || first + kTile - 1 > w.all.hi;
   };
   int k_ref = kFirstRef, v_ref = kFirstRef;
-  const bool odd = DP != D || LP * 16 != DP;
 
   // The tile's share into LDS as fp16 under the references (mixed: keys under
   // their own, values as bf16).
@@ -169,17 +186,16 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
       for (int p = 0; p < PASSES; p++) absent |= !d.ok[p];
     }
     absent = __builtin_amdgcn_ballot_w64(absent) != 0;
-    if (absent || odd) {
+    if (absent) {
 #pragma unroll
       for (int p = 0; p < PASSES; p++) {
-        if (!d.ok[p] || !has) {
+        if (!d.ok[p]) {
 #pragma unroll
           for (int i = 0; i < W; i++) d.k[p][i] = d.v[p][i] = 0;
           d.ks[p] = d.vs[p] = 0;
         }
       }
     }
-    const bool writes = LP * 16 == DP || 16 * sub < DP;
 #pragma unroll
     for (int p = 0; p < PASSES; p++) {
       const int n = kWaveKeys * wave + 64 / LP * p + lane_key;
@@ -190,25 +206,19 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
         k_base = 127 + X - own;
         nan |= has_nan<FMT>(d.v[p], d.vs[p]);
         if (sub == 0) powers[b][n] = d.ok[p] ? __builtin_ldexpf(1.0f, own - X - 127) : -1.0f;
-        if (writes) {
-          const float s = block_scale(d.vs[p], 0);
-          *reinterpret_cast<bf16x8 *>(v_to) = codes_operand_bf16<FMT>(&d.v[p][0], s);
-          *reinterpret_cast<bf16x8 *>(v_to + 16) = codes_operand_bf16<FMT>(&d.v[p][W / 2], s);
-        }
+        const float s = block_scale(d.vs[p], 0);
+        *reinterpret_cast<bf16x8 *>(v_to) = codes_operand_bf16<FMT>(&d.v[p][0], s);
+        *reinterpret_cast<bf16x8 *>(v_to + 16) = codes_operand_bf16<FMT>(&d.v[p][W / 2], s);
       } else {
         k_top = max(k_top, scale_rank(d.ks[p]));
         v_top = max(v_top, scale_rank(d.vs[p]));
-        if (writes) {
-          const float s = block_scale(d.vs[p], 127 + X - v_ref);
-          *reinterpret_cast<half8_t *>(v_to) = codes_operand<FMT>(&d.v[p][0], s);
-          *reinterpret_cast<half8_t *>(v_to + 16) = codes_operand<FMT>(&d.v[p][W / 2], s);
-        }
+        const float s = block_scale(d.vs[p], 127 + X - v_ref);
+        *reinterpret_cast<half8_t *>(v_to) = codes_operand<FMT>(&d.v[p][0], s);
+        *reinterpret_cast<half8_t *>(v_to + 16) = codes_operand<FMT>(&d.v[p][W / 2], s);
       }
-      if (writes) {
-        const float s = block_scale(d.ks[p], k_base);
-        *reinterpret_cast<half8_t *>(k_to) = codes_operand<FMT>(&d.k[p][0], s);
-        *reinterpret_cast<half8_t *>(k_to + 16) = codes_operand<FMT>(&d.k[p][W / 2], s);
-      }
+      const float s = block_scale(d.ks[p], k_base);
+      *reinterpret_cast<half8_t *>(k_to) = codes_operand<FMT>(&d.k[p][0], s);
+      *reinterpret_cast<half8_t *>(k_to + 16) = codes_operand<FMT>(&d.k[p][W / 2], s);
     }
     uint32_t word = 0;
     if (mixed) {
@@ -220,6 +230,30 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
       if (absent) word |= kAbsent;
     }
     if (lane == 0) staged[b][wave] = word;
+  };
+  // The same without a branch, for keys that are all there and all seen; a NaN
+  // block counts as a scale above the reference.
+  const int to_key = kWaveKeys * wave + lane_key;
+  const auto stage_fast = [&](int b) __attribute__((always_inline)) {
+    uint32_t k_top = 0, v_top = 0;
+    uint8_t *const k_to = k_lds[b] + to_key * KS + 32 * sub, *const v_to = v_lds[b] + to_key * VS + 32 * sub;
+    const int k_base = 127 + X - k_ref, v_base = 127 + X - v_ref;
+#pragma unroll
+    for (int p = 0; p < PASSES; p++) {
+      const float f = __builtin_bit_cast(float, (uint32_t)(max((int)d.ks[p], -k_base) + k_base) << 23);
+      const float g = __builtin_bit_cast(float, (uint32_t)(max((int)d.vs[p], -v_base) + v_base) << 23);
+      k_top = max(k_top, (uint32_t)d.ks[p]);
+      v_top = max(v_top, (uint32_t)d.vs[p]);
+      *reinterpret_cast<half8_t *>(k_to + 64 / LP * p * KS) = codes_operand<FMT>(&d.k[p][0], f);
+      *reinterpret_cast<half8_t *>(k_to + 64 / LP * p * KS + 16) = codes_operand<FMT>(&d.k[p][W / 2], f);
+      *reinterpret_cast<half8_t *>(v_to + 64 / LP * p * VS) = codes_operand<FMT>(&d.v[p][0], g);
+      *reinterpret_cast<half8_t *>(v_to + 64 / LP * p * VS + 16) = codes_operand<FMT>(&d.v[p][W / 2], g);
+    }
+    uint32_t word = 0;
+    word |= __builtin_amdgcn_ballot_w64((int)k_top > k_ref || (int)v_top > v_ref) != 0 ? kOver : 0;
+    word |= k_ref == kLastRef || __builtin_amdgcn_ballot_w64((int)k_top + 8 >= k_ref) != 0 ? kNearK : 0;
+    word |= v_ref == kLastRef || __builtin_amdgcn_ballot_w64((int)v_top + 8 >= v_ref) != 0 ? kNearV : 0;
+    staged[b][wave] = word;  // by all lanes
   };
 
   f32x16 acc[2 * ND];
@@ -240,16 +274,15 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
     return s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
   };
   const auto scores = [&](int b, f32x16 (&s)[2]) __attribute__((always_inline)) {
+    const f32x16 zeros = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-    for (int j = 0; j < 2; j++) {
+    for (int n = 0; n < DP / 16; n++) {
 #pragma unroll
-      for (int i = 0; i < 16; i++) s[j][i] = 0.0f;
-#pragma unroll
-      for (int n = 0; n < DP / 16; n++) {
+      for (int j = 0; j < 2; j++) {
         const half8_t k = *reinterpret_cast<const half8_t *>(k_lds[b] + k_at + 32 * j * KS + 32 * n);
 #pragma unroll
         for (int p = 0; p < NP; p++)
-          s[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[p][n], s[j], 0, 0, 0);
+          s[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[p][n], n + p == 0 ? zeros : s[j], 0, 0, 0);
       }
     }
   };
@@ -272,9 +305,11 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
     return (m == kMinusInf ? 0.0f : m) - kWeightExponent;
   };
 
-  const auto compute = [&](int b) __attribute__((always_inline)) {
+  // AND_NEXT: the next tile is staged among the scores' products
+  const auto compute = [&](int b, auto and_next) __attribute__((always_inline)) {
     f32x16 s[2];
     scores(b, s);
+    if constexpr (decltype(and_next)::value) stage_fast(b ^ 1);
     const float c = __builtin_ldexpf(row_scale, k_ref - X - 127);
     float mx = s[0][0];
 #pragma unroll
@@ -376,7 +411,7 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
     uint32_t top = 0;
 #pragma unroll
     for (int p = 0; p < PASSES; p++)
-      top = pk_max(top, d.ok[WHOLE ? 0 : p] && has ? scale_rank(d.ks[p]) | scale_rank(d.vs[p]) << 16 : 0);
+      top = pk_max(top, d.ok[WHOLE ? 0 : p] ? scale_rank(d.ks[p]) | scale_rank(d.vs[p]) << 16 : 0);
     top = wave_pk_max(top);
     if (lane == 0) tops[wave] = top;
     __syncthreads();
@@ -420,14 +455,23 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
         any = (uint32_t)__builtin_amdgcn_readfirstlane((int)(words[0] | words[1] | words[2] | words[3]));
       }
     }
-    if (t + 1 < w.last) {
-      stage(t + 1, is_mixed(t + 1));
-      if (t + 2 < w.last) load(t + 2);
+    const bool sees = active && max(first, one.lo) <= min(first + kTile - 1, two.hi);
+    bool there = true;
+    for (int p = 0; p < (WHOLE ? 1 : PASSES); p++) there &= d.ok[p];
+    if (sees && !mixed && t + 1 < w.last && !is_mixed(t + 1) && __builtin_amdgcn_ballot_w64(!there) == 0) {
+      compute(b, std::true_type{});
+      load(t + 2);  // in a branch, it would be waited for where the branches meet
       load_pages(t + 3);
-    }
-    if (active && max(first, one.lo) <= min(first + kTile - 1, two.hi)) {
-      if (mixed) compute_mixed(b, first, (any & kNan) != 0);
-      else compute(b);
+    } else {
+      if (t + 1 < w.last) {
+        stage(t + 1, is_mixed(t + 1));
+        load(t + 2);  // in a branch, it would be waited for where the branches meet
+        load_pages(t + 3);
+      }
+      if (sees) {
+        if (mixed) compute_mixed(b, first, (any & kNan) != 0);
+        else compute(b, std::false_type{});
+      }
     }
     __syncthreads();
   }
