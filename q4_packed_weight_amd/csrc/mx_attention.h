@@ -279,28 +279,26 @@ template <int W> __device__ __forceinline__ void load_codes(const uint8_t *p, ui
   }
 }
 
-// The scale bytes of a lane's blocks 2 p + g / 2 of a row: as loaded (whole
-// dwords of four blocks where rows are made of them, else bytes), and, once
-// settled, two to a dword.
+// The scale bytes of a lane's blocks 2 p + g / 2 of a row: as loaded (FOURS:
+// whole dwords of four blocks, for rows made of them; else bytes), and, once
+// settled, two to a dword.  Both ways in one kernel, by a branch, would be waited
+// for where the branches meet, and so would all loads before them.
 struct __attribute__((packed)) Packed4 { uint32_t v; };  // at any alignment
-template <int ND> struct RawScales {
+template <int ND, bool FOURS> struct RawScales {
   static constexpr int S = (ND + 1) / 2;
-  uint32_t raw[ND], pair[S];
-  __device__ __forceinline__ void load(const uint8_t *row, int nb, int g, bool fours) {
-    if (fours) {
+  uint32_t raw[FOURS ? S : ND], pair[S];
+  __device__ __forceinline__ void load(const uint8_t *row, int nb, int g) {
 #pragma unroll
-      for (int i = 0; i < ND; i++)
-        raw[i] = i & 1 ? 0 : reinterpret_cast<const Packed4 *>(row + 2 * i)->v;
-    } else {
-#pragma unroll
-      for (int p = 0; p < ND; p++) raw[p] = row[min(2 * p + (g >> 1), nb - 1)];
+    for (int i = 0; i < (FOURS ? S : ND); i++) {
+      if constexpr (FOURS) raw[i] = reinterpret_cast<const Packed4 *>(row + 4 * i)->v;
+      else raw[i] = row[min(2 * i + (g >> 1), nb - 1)];
     }
   }
-  __device__ __forceinline__ void settle(int g, bool fours) {
+  __device__ __forceinline__ void settle(int g) {
 #pragma unroll
     for (int i = 0; i < S; i++) {
-      const uint32_t bytes = 2 * i + 1 < ND ? raw[2 * i] | raw[2 * i + 1 < ND ? 2 * i + 1 : 0] << 16 : raw[2 * i];
-      pair[i] = fours ? raw[2 * i] >> (8 * (g >> 1)) & 0x00FF00FFu : bytes;
+      if constexpr (FOURS) pair[i] = raw[i] >> (8 * (g >> 1)) & 0x00FF00FFu;
+      else pair[i] = raw[2 * i] | (2 * i + 1 < ND ? raw[2 * i + 1 < ND ? 2 * i + 1 : 0] << 16 : 0);
     }
   }
   // 2^(s + base - 127), s + base <= 254; NaN blocks as any others

@@ -13,10 +13,10 @@ constexpr int kStepKeys = 32;
 
 // One wave's 32 keys (lane: key l % 16 of two tiles, group g = l / 16 of its
 // dims: 64 p + 16 g .. + 15 for p < ND) as they lie in memory.
-template <int FMT, int ND> struct StepData {
+template <int FMT, int ND, bool FOURS> struct StepData {
   static constexpr int W = FMT == MX_FP8 ? 4 : 2;  // dwords of 16 codes
   uint32_t k[2][ND][W], v[2][ND][W];
-  RawScales<ND> ks[2], vs[2];
+  RawScales<ND, FOURS> ks[2], vs[2];
   uint32_t ok;  // bit by key, the same in every lane
 };
 
@@ -34,7 +34,7 @@ constexpr int kWavesPerSimd = ND == 1 ? 5 : ND == 2 ? (NP == 1 ? 4 : 3) : ND == 
 // and in LDS, the next one's are sent for, and its weights and sums are made
 // while they come.  The four results, and those of the ranges, are joined by
 // their largest x.
-template <int NP, int FMT, int ND, bool MIXED>
+template <int NP, int FMT, int ND, bool MIXED, bool FOURS>
 __global__ __launch_bounds__(kWaves * 64, MIXED ? 1 : (kWavesPerSimd<NP, ND>)) void attention_rows_kernel(AttentionArgs a) {
   constexpr int DP = 64 * ND;                // dims, padded
   constexpr int VS = 2 * DP + 32;            // bytes of a key's row of V in LDS
@@ -79,8 +79,8 @@ __global__ __launch_bounds__(kWaves * 64, MIXED ? 1 : (kWavesPerSimd<NP, ND>)) v
   }
   // Every lane loads, absent keys and dims row 0 of their head and dims 0 of
   // their row, without a branch; fill_in puts zeros there.
-  const bool odd = (D & 32) != 0, fours = nb % 4 == 0;
-  StepData<FMT, ND> d;
+  const bool odd = (D & 32) != 0;
+  StepData<FMT, ND, FOURS> d;
   const auto load_step = [&](int step, const int (&page)[2]) __attribute__((always_inline)) {
     uint32_t okay = 0;
 #pragma unroll
@@ -98,16 +98,16 @@ __global__ __launch_bounds__(kWaves * 64, MIXED ? 1 : (kWavesPerSimd<NP, ND>)) v
         load_codes(a.k_codes + at + c, d.k[j][p]);
         load_codes(a.v_codes + at + c, d.v[j][p]);
       }
-      d.ks[j].load(a.k_scales + s_at, nb, g, fours);
-      d.vs[j].load(a.v_scales + s_at, nb, g, fours);
+      d.ks[j].load(a.k_scales + s_at, nb, g);
+      d.vs[j].load(a.v_scales + s_at, nb, g);
     }
     d.ok = (uint32_t)__builtin_amdgcn_readfirstlane((int)okay);
   };
   const auto fill_in = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < 2; j++) {
-      d.ks[j].settle(g, fours);
-      d.vs[j].settle(g, fours);
+      d.ks[j].settle(g);
+      d.vs[j].settle(g);
     }
     if (d.ok != 0xFFFFFFFFu || odd) {
 #pragma unroll
@@ -117,7 +117,7 @@ __global__ __launch_bounds__(kWaves * 64, MIXED ? 1 : (kWavesPerSimd<NP, ND>)) v
         for (int p = 0; p < ND; p++) {
           if (!ok || !has[p]) {
 #pragma unroll
-            for (int i = 0; i < StepData<FMT, ND>::W; i++) d.k[j][p][i] = d.v[j][p][i] = 0;
+            for (int i = 0; i < StepData<FMT, ND, FOURS>::W; i++) d.k[j][p][i] = d.v[j][p][i] = 0;
             d.ks[j].clear(p);
             d.vs[j].clear(p);
           }
@@ -171,7 +171,7 @@ __global__ __launch_bounds__(kWaves * 64, MIXED ? 1 : (kWavesPerSimd<NP, ND>)) v
   typedef __attribute__((address_space(3))) s16x4 LdsS16x4;
   const uint8_t *const read_at = mem + (4 * g + (r16 >> 2)) * VS + 8 * (r16 & 3);
   constexpr int X = kCodeExponent<FMT>;
-  constexpr int W = StepData<FMT, ND>::W;
+  constexpr int W = StepData<FMT, ND, FOURS>::W;
 
   // 16 dims of 32 values, transposed
   const auto value_operand = [&](int t) __attribute__((always_inline)) {
@@ -500,6 +500,19 @@ int slots(const AttentionArgs &a) {
   if (tiled(a)) return 256 * (nd <= 2 ? 2 : 1);
   return 256 * (nd <= 2 ? 4 : 2);
 }
+template <int NP, int FMT, int ND>
+void launch_rows(const AttentionArgs &a, int blocks, hipStream_t stream) {
+  const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(blocks), dim3(256), 0, stream, a); };
+  if constexpr (ND % 2 == 0) {
+    if (a.head_dim % 128 == 0) {
+      if (a.max_queries == 1) go(attention_rows_kernel<NP, FMT, ND, false, true>);
+      else go(attention_rows_kernel<NP, FMT, ND, true, true>);
+      return;
+    }
+  }
+  if (a.max_queries == 1) go(attention_rows_kernel<NP, FMT, ND, false, false>);
+  else go(attention_rows_kernel<NP, FMT, ND, true, false>);
+}
 constexpr int kMaxPlanned = 512;  // sequences that every workgroup looks through
 
 }  // namespace
@@ -539,13 +552,8 @@ hipError_t mx_attention_launch(const AttentionArgs &a, hipStream_t stream) {
     e = attention_tiled_launch(a, blocks, stream);
   } else {
     const int nd = (a.head_dim + 63) / 64;
-#define GO(NP, F, ND)                                                                            \
-  if (a.max_queries == 1)                                                                        \
-    hipLaunchKernelGGL((attention_rows_kernel<NP, F, ND, false>), dim3(blocks), dim3(256), 0,    \
-                       stream, a);                                                               \
-  else                                                                                           \
-    hipLaunchKernelGGL((attention_rows_kernel<NP, F, ND, true>), dim3(blocks), dim3(256), 0,     \
-                       stream, a)
+#define GO(NP, F, ND)                                                                           \
+  launch_rows<NP, F, ND>(a, blocks, stream)
 #define BY_DIM(NP, F)                    \
   switch (nd) {                          \
     case 1: GO(NP, F, 1); break;         \
