@@ -12,10 +12,10 @@
 //            keys taken together, so that the largest code still fits: exact
 //            for blocks whose scale lies up to 2^21 (MX_FP8) or 2^36 (MX_FP4)
 //            below it, as fp16's subnormals reach, and these operands keep them.
-//   weights  p = exp2(x - largest x + 10), in (0, 2^10]: one fp16, off by 2^-11
-//            of p, an eighth of what bf16 would leave of it; for fp32 a second
-//            one for what is left (2^-23).  The sums of p are of the unrounded
-//            ones, in fp32.
+//   weights  p = exp2(x - m + 10) with m the largest x so far or up to 4 less, so at
+//            most 2^14: one fp16, off by 2^-11 of p, an eighth of what bf16 would
+//            leave of it; for fp32 a second one for what is left (2^-23).  The sums
+//            of p are of the unrounded ones, in fp32.
 // Keys that some rows see and others do not (a causal chunk's own, a window's
 // edge) are taken without a common reference, which a key that a row does not
 // see would give it: each key's own for its scores, and bf16 for its values,
@@ -36,7 +36,7 @@ typedef short i16x2 __attribute__((ext_vector_type(2)));
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 
 constexpr float kMinusInf = -__builtin_inff();
-constexpr int kWeightExponent = 10;
+constexpr int kWeightExponent = 10;  // and up to 4 more
 // The power that the largest code takes within fp16: 448 * 2^6, 6 * 2^13.
 template <int FMT> constexpr int kCodeExponent = FMT == MX_FP8 ? 6 : 13;
 

@@ -32,8 +32,12 @@ constexpr int kWavesPerSimd = ND == 1 ? 5 : ND == 2 ? (NP == 1 ? 4 : 3) : ND == 
 // as fp16, each wave its own 32 keys, and comes back transposed.  A wave takes
 // every fourth step of its workgroup's range; once a step's codes are operands
 // and in LDS, the next one's are sent for, and its weights and sums are made
-// while they come.  The four results, and those of the ranges, are joined by
-// their largest x.
+// while they come.  The four results, and those of the shares, are joined by
+// their largest x.  Bound by memory and, for small batches, by its latency: 64
+// tokens over 1024 .. 8192 keys of 8 heads of 128 (MX_FP8, 621 MB) 150 us, 4.1 TB/s;
+// 2 tokens over 131072 keys in MX_FP4 (213 MB) 62 us; one over 1000 keys 10.7 us, of
+// which the join is 4: starts, pages and codes are three loads that wait for one
+// another, and a step alone on its SIMD takes 1.5 us.
 template <int NP, int FMT, int ND, bool MIXED, bool FOURS>
 __global__ __launch_bounds__(kWaves * 64, MIXED ? 1 : (kWavesPerSimd<NP, ND>)) void attention_rows_kernel(AttentionArgs a) {
   constexpr int DP = 64 * ND;                // dims, padded
@@ -443,12 +447,17 @@ __global__ __launch_bounds__(kWaves * 64, MIXED ? 1 : (kWavesPerSimd<NP, ND>)) v
   }
 }
 
+// Rows of a workgroup of the join: one a wave of the few, four of the many, whose
+// workgroups take longer to start than to work (mixed batch of 52 tiles and 5 heads
+// 13 us, with two rows 20).
+constexpr int join_rows(int rows) { return rows == kRows ? 4 : 16; }
+
 // The shares' results joined, a wave to a row: the weights of 64 shares at a
 // time, then four dims of every second share to a lane (of all for head_dim
 // above 128, of every fourth up to 64).
 template <int ROWS, int KEYS>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a) {
-  constexpr int kChunk = ROWS == kRows ? 4 : 16;  // rows of a workgroup
+  constexpr int kChunk = join_rows(ROWS);
   Work w;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, D = a.head_dim;
   if (!work_of<ROWS, KEYS, true>(a, blockIdx.x, w) || w.splits == 1 ||
@@ -462,7 +471,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a) {
     const int head = w.kv_head * a.group + row - token * a.group;
     const int64_t part = part_row<ROWS>(a, w, 0, r);
     const float2 *const stats = part_stats(a) + part;
-    const f32x4 *const values = reinterpret_cast<const f32x4 *>(a.partial + part * D) + c;
+    const f32x4 *const values = reinterpret_cast<const f32x4 *>(a.partial + part * D) + min(c, columns - 1);
     float m = kMinusInf, total = 0.0f;
     f32x4 v = {0, 0, 0, 0};
     for (int from = 0; from < w.splits; from += 64) {
@@ -472,12 +481,21 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a) {
 #pragma unroll
       for (int i = 1; i < 64; i *= 2) most = fmaxf(most, __shfl_xor(most, i));
       most = fmaxf(most, m);
-      const float share = part_share(mine.x, most), before = part_share(m, most);
+      const float share = lane < n ? part_share(mine.x, most) : 0.0f, before = part_share(m, most);
       total = total * before + group_sum<64>(share * mine.y);
       v *= before;
-      for (int i = 0; i < n; i += groups) {
-        const float f = __shfl(share, (i + g) & 63);
-        if (i + g < n && c < columns) v += f * values[(from + i + g) * stride * columns];
+      // eight parts on their way at a time; those behind the last are the last, times 0
+      for (int i = g; i - g < n; i += 8 * groups) {
+        f32x4 part[8];
+#pragma unroll
+        for (int k = 0; k < 8; k++)
+          part[k] = values[(from + min(i + k * groups, n - 1)) * stride * columns];
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+          const int at = i + k * groups;
+          const float f = __shfl(share, at & 63);
+          v += (at < n ? f : 0.0f) * part[k];
+        }
       }
       m = most;
     }
@@ -574,7 +592,7 @@ hipError_t mx_attention_launch(const AttentionArgs &a, hipStream_t stream) {
   const int64_t rows = (int64_t)a.max_queries * a.group;
   const int64_t tiles = std::min((int64_t)a.n_seqs * a.tiles,
                                  (int64_t)a.n_tokens * a.group / (tiled(a) ? kTiledRows : kRows) + a.n_seqs);
-  const int chunk = tiled(a) ? 16 : 4;
+  const int chunk = join_rows(tiled(a) ? kTiledRows : kRows);
   const dim3 grid((uint32_t)(tiles * a.n_kv_heads),
                   (uint32_t)((std::min<int64_t>(rows, tiled(a) ? kTiledRows : kRows) + chunk - 1) / chunk));
   if (tiled(a))

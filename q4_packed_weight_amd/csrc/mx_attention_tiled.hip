@@ -43,8 +43,21 @@ template <int LP> __device__ __forceinline__ uint32_t max_of_key(uint32_t v) {
   return v;
 }
 
+// As in the form for few rows, scores are S^T = K Q^T and the sums O^T += V^T P^T,
+// here of 32 keys by 32 rows: a row's statistics are two lanes' own, and sixteen of
+// a lane's weights are two operands as they stand.  The four waves stage a tile of
+// 64 keys once for their 128 rows, 16 keys each, converted on the way into LDS (a
+// conversion of two codes a lane is one instruction, and each is made once instead
+// of by every wave); two tiles in LDS and one in registers, two workgroups a CU.
+// The tile's references are those of the tiles before as long as they hold (stage
+// says so, stage_again mends it), so that nothing is exchanged before the barrier.
+// Bound by the waits of two waves a SIMD: of 2048 tokens over 8192 keys (32 heads of
+// 128, 241 GFLOP, 322 us, 0.75 PFLOP/s, half of a large fp16 product's rate) the
+// matrix pipe works 27% and the vector unit 40% of the time.  Tried: operands read
+// ahead in a fixed order, with the sums kept in memory around that loop so that its
+// registers suffice 361 us, without 390; 2 x 32-key halves 477.
 // WHOLE: pages of a multiple of 16 keys, so that a wave's 16 lie in one and
-// their addresses are scalars.
+// their addresses are scalars (351 against 341 us when it came).
 template <int NP, int FMT, int ND, bool WHOLE>
 __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_kernel(AttentionArgs a) {
   constexpr int DP = 64 * ND;

@@ -210,3 +210,18 @@ def test_a_prompt_then_single_tokens(fmt):
         x.normal_()
         graph.replay()
         check(b, held[1], held[2])
+
+
+def test_the_example_runs():
+    """Its y against 64 bits: bf16's rounding, 2^-8 at most, and no more than as much
+    again for weights and sums."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "mx_attention.py")
+    spec = importlib.util.spec_from_file_location("mx_attention_example", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    errors = example.main(["--batch", "2", "--prompt", "40", "--tokens", "5", "--dim", "256", "--heads",
+                           "4", "--kv-heads", "2", "--head-dim", "64"])
+    assert max(errors) <= 2.0 ** -7
