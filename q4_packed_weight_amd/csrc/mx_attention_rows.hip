@@ -457,7 +457,7 @@ constexpr int join_rows(int rows) { return rows == kRows ? 4 : 16; }
 // above 128, of every fourth up to 64).
 template <int ROWS, int KEYS>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a) {
-  constexpr int kChunk = join_rows(ROWS);
+  constexpr int kChunk = join_rows(ROWS), kWide = ROWS == kRows ? 8 : 2;  // many rows: few shares
   Work w;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, D = a.head_dim;
   if (!work_of<ROWS, KEYS, true>(a, blockIdx.x, w) || w.splits == 1 ||
@@ -484,14 +484,14 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a) {
       const float share = lane < n ? part_share(mine.x, most) : 0.0f, before = part_share(m, most);
       total = total * before + group_sum<64>(share * mine.y);
       v *= before;
-      // eight parts on their way at a time; those behind the last are the last, times 0
-      for (int i = g; i - g < n; i += 8 * groups) {
-        f32x4 part[8];
+      // kWide parts on their way at a time; those behind the last are the last, times 0
+      for (int i = g; i - g < n; i += kWide * groups) {
+        f32x4 part[kWide];
 #pragma unroll
-        for (int k = 0; k < 8; k++)
+        for (int k = 0; k < kWide; k++)
           part[k] = values[(from + min(i + k * groups, n - 1)) * stride * columns];
 #pragma unroll
-        for (int k = 0; k < 8; k++) {
+        for (int k = 0; k < kWide; k++) {
           const int at = i + k * groups;
           const float f = __shfl(share, at & 63);
           v += (at < n ? f : 0.0f) * part[k];
