@@ -35,7 +35,7 @@ constexpr int kWavesPerSimd = ND == 1 ? 5 : ND == 2 ? (NP == 1 ? 4 : 3) : ND == 
 // while they come.  The four results, and those of the shares, are joined by
 // their largest x.  Bound by memory and, for small batches, by its latency: 64
 // tokens over 1024 .. 8192 keys of 8 heads of 128 (MX_FP8, 621 MB) 150 us, 4.1 TB/s;
-// 2 tokens over 131072 keys in MX_FP4 (213 MB) 62 us; one over 1000 keys 10.7 us, of
+// 2 tokens over 131072 keys in MX_FP4 (213 MB) 56 us; one over 1000 keys 10.5 us, of
 // which the join is 4: starts, pages and codes are three loads that wait for one
 // another, and a step alone on its SIMD takes 1.5 us.
 template <int NP, int FMT, int ND, bool MIXED, bool FOURS>

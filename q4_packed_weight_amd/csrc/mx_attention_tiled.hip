@@ -53,7 +53,7 @@ template <int LP> __device__ __forceinline__ uint32_t max_of_key(uint32_t v) {
 // says so, stage_again mends it), so that nothing is exchanged before the barrier.
 // Bound by the waits of two waves a SIMD: of 2048 tokens over 8192 keys (32 heads of
 // 128, 241 GFLOP, 322 us, 0.75 PFLOP/s, half of a large fp16 product's rate) the
-// matrix pipe works 27% and the vector unit 40% of the time.  Tried: operands read
+// matrix pipe works 28% and the vector unit 43% of the time.  Tried: operands read
 // ahead in a fixed order, with the sums kept in memory around that loop so that its
 // registers suffice 361 us, without 390; 2 x 32-key halves 477.
 // WHOLE: pages of a multiple of 16 keys, so that a wave's 16 lie in one and
