@@ -291,8 +291,9 @@ int mx_cache_read(const int64_t *slots, int64_t n_tokens, int64_t n_heads, int64
  *   q          exact for bf16 and fp16; fp32 as two fp16 values, off by 2^-23
  *              of each; below 2^-29 of a row's largest bits are lost
  *   k, v       exact where the scale bytes of the keys taken together (32 or
- *              64 in a row) lie within 21 (MX_FP8) or 36 (MX_FP4) of their
- *              largest, values above 2^-55; lower ones lose bits
+ *              64 in a row) lie within 13 (MX_FP8) or 28 (MX_FP4) of their
+ *              largest and that above 2^-55; lower blocks lose bits, from the
+ *              lowest on
  *   w          off by 2^-11 of each (bf16 and fp16), 2^-23 (fp32)
  * The order of the sums depends on the sizes, starts and counts alone.
  */

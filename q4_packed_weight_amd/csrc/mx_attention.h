@@ -9,9 +9,10 @@
 //            the value).  What lies 2^-29 below the row's
 //            largest is lost bit by bit.
 //   keys and values  code * 2^(s - ref), ref the largest scale byte among the
-//            keys taken together, so that the largest code still fits: exact
-//            for blocks whose scale lies up to 2^21 (MX_FP8) or 2^36 (MX_FP4)
-//            below it, as fp16's subnormals reach, and these operands keep them.
+//            keys taken together or up to 8 above it, so that the largest code
+//            still fits: exact for blocks whose scale lies up to 2^21 (MX_FP8) or
+//            2^36 (MX_FP4) below ref, as fp16's subnormals reach, and these
+//            operands keep them.
 //   weights  p = exp2(x - m + 10) with m the largest x so far or up to 4 less, so at
 //            most 2^14: one fp16, off by 2^-11 of p, an eighth of what bf16 would
 //            leave of it; for fp32 a second one for what is left (2^-23).  The sums
