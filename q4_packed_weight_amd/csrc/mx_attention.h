@@ -390,6 +390,17 @@ __device__ __forceinline__ float part_share(float m, float most) {
   return m == kMinusInf ? 1.0f : __builtin_amdgcn_exp2f(m - most);
 }
 
+// Before a row's sums are divided by those of its weights they are up to 2^44
+// (2^14 for each of 2^30 keys) times the largest value, which alone may be next to
+// fp32's largest: they are kept times 2^-44, and the quotient is put back.
+constexpr int kSumExponent = 44;
+__device__ __forceinline__ f32x4 quotient(f32x4 v, float sum) {
+  v *= sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+  for (int i = 0; i < 4; i++) v[i] = __builtin_ldexpf(v[i], kSumExponent);
+  return v;
+}
+
 // 128 rows a workgroup, 64 keys a step.
 constexpr int kTiledRows = 128, kTiledKeys = 64;
 hipError_t attention_tiled_launch(const AttentionArgs &a, int blocks, hipStream_t stream);

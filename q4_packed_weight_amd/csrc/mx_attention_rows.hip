@@ -405,7 +405,7 @@ __global__ __launch_bounds__(kWaves * 64, MIXED ? 1 : (kWavesPerSimd<NP, ND>)) v
       compute(step);
   }
 
-  // the waves' results, each as it stands before its power is put back
+  // the waves' results, under one power
   l = add_partner_row<64>(add_partner_row<32>(l));
   float *const o = reinterpret_cast<float *>(mem) + r16 * OS;
 #pragma unroll
@@ -413,7 +413,7 @@ __global__ __launch_bounds__(kWaves * 64, MIXED ? 1 : (kWavesPerSimd<NP, ND>)) v
     f32x4 v = acc[t];
 #pragma unroll
     for (int i = 0; i < 4; i++)
-      v[i] = __builtin_ldexpf(v[i], v_ref - kCodeExponent<FMT> - 127);
+      v[i] = __builtin_ldexpf(v[i], v_ref - kCodeExponent<FMT> - 127 - kSumExponent);
     *reinterpret_cast<f32x4 *>(o + 16 * t + 4 * g) = v;
   }
   if (g == 0) stats[wave][r16] = make_float2(m, l);
@@ -439,8 +439,8 @@ __global__ __launch_bounds__(kWaves * 64, MIXED ? 1 : (kWavesPerSimd<NP, ND>)) v
     for (int i = 0; i < kWaves; i++)
       v += share[i] * *reinterpret_cast<const f32x4 *>(lds + i * kRegion + (out * OS + c) * 4);
     if (whole) {
-      v *= sum == 0.0f ? 0.0f : 1.0f / sum;
-      store_y4(a, (int64_t)(w.seq.q0 + out_token) * a.y_stride + (int64_t)head * D + c, v);
+      store_y4(a, (int64_t)(w.seq.q0 + out_token) * a.y_stride + (int64_t)head * D + c,
+               quotient(v, sum));
     } else {
       *reinterpret_cast<f32x4 *>(a.partial + part * D + c) = v;
     }
@@ -505,7 +505,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a) {
     }
     if (g == 0 && c < columns)
       store_y4(a, (int64_t)(w.seq.q0 + token) * a.y_stride + (int64_t)head * D + 4 * c,
-               v * (total == 0.0f ? 0.0f : 1.0f / total));
+               quotient(v, total));
   }
 }
 

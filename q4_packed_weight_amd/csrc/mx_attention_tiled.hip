@@ -497,7 +497,6 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
   const bool whole = w.splits == 1;
   const int64_t part = part_row<kRows>(a, w, w.split, 32 * wave + r32);
   if (!whole && half == 0) part_stats(a)[part] = make_float2(m, l);
-  const float inv = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
 #pragma unroll
   for (int t = 0; t < 2 * ND; t++)
 #pragma unroll
@@ -505,9 +504,9 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
       const int c = 32 * t + 2 * i + 4 * half;
       f32x4 v;
 #pragma unroll
-      for (int n = 0; n < 4; n++) v[n] = __builtin_ldexpf(acc[t][i + n] * inv, v_ref - X - 127);
+      for (int n = 0; n < 4; n++) v[n] = __builtin_ldexpf(acc[t][i + n], v_ref - X - 127 - kSumExponent);
       if (32 * t < D) {
-        if (whole) store_y4(a, (int64_t)(w.seq.q0 + token) * a.y_stride + (int64_t)head * D + c, v);
+        if (whole) store_y4(a, (int64_t)(w.seq.q0 + token) * a.y_stride + (int64_t)head * D + c, quotient(v, l));
         else *reinterpret_cast<f32x4 *>(a.partial + part * D + c) = v;
       }
     }

@@ -1,0 +1,82 @@
+"""Attention over the quantised cache near the ends of fp32's range: values and
+scores that are finite, and give finite results.
+
+Bounds are those of test_mx_attention_gpu.py, and for the weights' operands, fp16
+whose subnormals are of 2^-24 beside a largest weight of at least 2^10, half a
+step of those: 2^-35 of the largest weight, or the weight itself where it is less.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import mx
+from test_mx_attention_gpu import TYPES, U, Batch, host, put, rounding
+
+pytestmark = pytest.mark.gpu
+
+WIDE = ["bf16", "fp32"]  # fp16 ends at 2^16
+# With so many sequences none has its keys cut into shares: a wave (few rows) or a
+# workgroup takes them one after the other.
+IN_ONE = [(0, 0)] * 600
+
+
+def values(b, i, array, x):
+    """x [keys][heads][head_dim] as sequence i's keys (0) or values (2)."""
+    assert x.shape == (len(b.slots[i]), b.Hk, b.D)
+    b.pool.put(array, b.slots[i], *mx.quantize(x, b.fmt))
+
+
+def reference(q, k, v, scale, sees):
+    """(y, sum of the weights' shares of |v|, of |v| by 2^-35 or the weight, the
+    largest score, the largest sum of |q||k|) in 64 bits."""
+    y, mass, low = (np.zeros(q.shape) for _ in range(3))
+    top, size = np.zeros(len(q)), np.zeros(len(q))
+    for r in range(len(q)):
+        j = np.nonzero(sees[r])[0]
+        if not len(j):
+            continue
+        x = (k[j] @ q[r]) * scale
+        w = np.exp(x - x.max())
+        w /= w.sum()
+        y[r], mass[r] = w @ v[j], w @ np.abs(v[j])
+        low[r] = np.minimum(w, 2.0 ** -35) @ np.abs(v[j])
+        top[r], size[r] = np.abs(x).max(), (np.abs(k[j]) @ np.abs(q[r])).max() * abs(scale)
+    return y, mass, low, top, size
+
+
+def check(b, y, causal=True, window=0, hidden=(), tokens=None):
+    """Sequence 0's tokens (all, or those given)."""
+    nq, nk = b.seqs[0]
+    tokens = np.arange(nq) if tokens is None else np.asarray(tokens)
+    a = int(b.starts[0])
+    y = host(y).reshape(b.T, b.Hk, b.G, b.D)
+    sees = b.sees(0, causal, window, hidden)[tokens].repeat(b.G, 0)
+    k, v = b.pool.values(0, b.slots[0]), b.pool.values(2, b.slots[0])
+    w = U if b.kind == "fp32" else 2.0 ** -11
+    for h in range(b.Hk):
+        rows = b.held[a + tokens].reshape(-1, b.Hk, b.G, b.D)[:, h].reshape(-1, b.D)
+        seen = sees.any(0)  # what no row sees may be anything
+        want, mass, low, top, size = reference(rows, k[seen, h], v[seen, h], b.scale, sees[:, seen])
+        off = ((b.D / 4 + 17) * size + 8 * top + 8) * U
+        rest = mass * (w + 2 * off[:, None] + (nk / 8 + 64) * U) + low
+        got = y[a + tokens, h].reshape(-1, b.D)
+        assert np.isfinite(want).all() and np.isfinite(got).all(), (h, np.argwhere(~np.isfinite(got))[:5])
+        bad = np.abs(got - want) > rounding(b.kind, np.abs(want) + rest) + rest
+        assert not bad.any(), (h, np.argwhere(bad)[:5], got[bad][:5], want[bad][:5])
+
+
+# one token and chunks, in one share of keys and in several
+SHAPES = [([(1, 64)], 4), ([(1, 4096)], 4), ([(4, 1024)], 2), ([(40, 256)], 2), ([(40, 4096)], 2)]
+
+
+@pytest.mark.parametrize("fmt", ["fp4", "fp8"])
+@pytest.mark.parametrize("kind", WIDE)
+@pytest.mark.parametrize("seqs,G", SHAPES)
+def test_values_near_the_largest(seqs, G, kind, fmt):
+    """Values to 2^127: their sums times the weights are beyond fp32, their mean is
+    not."""
+    b = Batch(seqs, 2, G, 64, 16, fmt, kind)
+    nk = seqs[0][1]
+    values(b, 0, 2, b.g.uniform(0.5, 1.0, (nk, 2, 64)) * b.g.choice([-1, 1, 1, 1], (nk, 2, 64)) * 2.0 ** 127)
+    b.pool.upload()
+    check(b, b.run(causal=False), causal=False, tokens=[0, seqs[0][0] // 2, seqs[0][0] - 1])
