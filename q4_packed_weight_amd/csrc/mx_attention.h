@@ -245,12 +245,27 @@ __device__ __forceinline__ float block_scale(uint32_t s, int base) {
 // A reference: that of the keys taken together, or the one before as long as it
 // is no lower and at most 2^8 above, so that it seldom changes.  What is summed up
 // carries the values'.  It may fall as well: a single large value takes no bits
-// from those of other keys.  Not below 64, or what was summed up at 2^59 could
-// leave fp32: keys and values below 2^-55 lose bits.
+// from those of other keys.  Not below 64, so that keys and values below 2^-55 lose
+// bits.
 constexpr int kFirstRef = 127, kLastRef = 64;
 __device__ __forceinline__ int reference(int before, int top) {
   const int now = max(top, kLastRef);
   return now > before || now + 8 < before ? now : before;
+}
+
+// Under one reference a sum is below 2^60 (2^44 of weights, 2^16 of codes), but what
+// was summed under a higher one grows by the fall, up to 2^190 of it.  Where a row's
+// largest sum, of magnitude bits `top`, would pass 2^126, its maximum is taken to be
+// higher by this power of two, and sums and sum of weights are made smaller by it:
+// its weights from there on are smaller too, and count for less than 2^-65 of what
+// there is.
+__device__ __forceinline__ int excess(uint32_t top, int fall) {
+  return max(0, (int)(top >> 23) + fall - 252);
+}
+// A sum's magnitude bits; what is not finite stays so, and holds nothing back.
+__device__ __forceinline__ uint32_t sum_bits(float v) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu;
+  return b >= 0x7F800000u ? 0 : b;
 }
 
 // Eight codes (two dwords of e4m3, one of e2m1) as a matrix operand.

@@ -211,11 +211,20 @@ __global__ __launch_bounds__(kWaves * 64, MIXED ? 1 : (kWavesPerSimd<NP, ND>)) v
     const bool up = mx > m + 4.0f;
     if (__builtin_amdgcn_ballot_w64(up) != 0 || v_new != v_ref) {
       const float f = up ? __builtin_amdgcn_exp2f(m - mx) : 1.0f;
-      l *= f;
-      const float o = __builtin_ldexpf(f, v_ref - v_new);
+      int power = v_ref - v_new, more = 0;
+      if (power > 0) {
+        uint32_t top = 0;
 #pragma unroll
-      for (int i = 0; i < 4 * ND; i++) acc[i] *= o;
-      m = up ? mx : m;
+        for (int i = 0; i < 16 * ND; i++) top = max(top, sum_bits(acc[i >> 2][i & 3]));
+        const float most = __builtin_bit_cast(float, swap_max_u32(top)) * f;
+        more = excess(__builtin_bit_cast(uint32_t, most), power);
+        power -= more;
+      }
+      l = __builtin_ldexpf(l * f, -more);
+#pragma unroll
+      for (int i = 0; i < 16 * ND; i++)
+        acc[i >> 2][i & 3] = __builtin_ldexpf(acc[i >> 2][i & 3] * f, power);
+      m = (up ? mx : m) + more;
       v_ref = v_new;
     }
     return (m == kMinusInf ? 0.0f : m) - kWeightExponent;

@@ -299,20 +299,35 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
       }
     }
   };
-  const auto scale_sums = [&](float f, int v_new) __attribute__((always_inline)) {
-    l *= f;
-    const float o = __builtin_ldexpf(f, v_ref - v_new);
+  // what was summed to the values' new reference
+  const auto refer = [&](int v_new) __attribute__((always_inline)) {
+    int power = v_ref - v_new;
+    if (power > 0) {
+      uint32_t top = 0;
 #pragma unroll
-    for (int t = 0; t < 2 * ND; t++)
+      for (int i = 0; i < 32 * ND; i++) top = max(top, sum_bits(acc[i >> 4][i & 15]));
+      const auto y = __builtin_amdgcn_permlane32_swap(top, top, false, false);
+      const uint32_t y0 = y[0], y1 = y[1];
+      const int more = excess(max(y0, y1), power);
+      m += more;
+      l = __builtin_ldexpf(l, -more);
+      power -= more;
+    }
 #pragma unroll
-      for (int i = 0; i < 16; i++) acc[t][i] *= o;
+    for (int i = 0; i < 32 * ND; i++) acc[i >> 4][i & 15] = __builtin_ldexpf(acc[i >> 4][i & 15], power);
+    v_ref = v_new;
   };
   // as in the form for few rows: a maximum up to 2^4 too low stays
   const auto raise = [&](float mx) __attribute__((always_inline)) {
     mx = swap_max32(mx);
     const bool up = mx > m + 4.0f;
     if (__builtin_amdgcn_ballot_w64(up) != 0) {
-      scale_sums(up ? __builtin_amdgcn_exp2f(m - mx) : 1.0f, v_ref);
+      const float f = up ? __builtin_amdgcn_exp2f(m - mx) : 1.0f;
+      l *= f;
+#pragma unroll
+      for (int t = 0; t < 2 * ND; t++)
+#pragma unroll
+        for (int i = 0; i < 16; i++) acc[t][i] *= f;
       m = up ? mx : m;
     }
     return (m == kMinusInf ? 0.0f : m) - kWeightExponent;
@@ -432,9 +447,7 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
       top = pk_max(pk_max(tops[0], tops[1]), pk_max(tops[2], tops[3]));
       top = (uint32_t)__builtin_amdgcn_readfirstlane((int)top);
       k_ref = reference(k_ref, top & 0xFFFF);
-      const int v_new = reference(v_ref, top >> 16);
-      scale_sums(1.0f, v_new);
-      v_ref = v_new;
+      refer(reference(v_ref, top >> 16));
     }
     stage(t, absent);
     __syncthreads();

@@ -80,3 +80,39 @@ def test_values_near_the_largest(seqs, G, kind, fmt):
     values(b, 0, 2, b.g.uniform(0.5, 1.0, (nk, 2, 64)) * b.g.choice([-1, 1, 1, 1], (nk, 2, 64)) * 2.0 ** 127)
     b.pool.upload()
     check(b, b.run(causal=False), causal=False, tokens=[0, seqs[0][0] // 2, seqs[0][0] - 1])
+
+
+@pytest.mark.parametrize("fmt", ["fp4", "fp8"])
+@pytest.mark.parametrize("kind", WIDE)
+@pytest.mark.parametrize("power", [20, 40, 60, 100, 120])
+@pytest.mark.parametrize("seqs,G", [([(1, 1536)], 4), ([(3, 1536)], 4), ([(40, 1536)], 2)])
+def test_large_values_before_small_ones(seqs, G, power, kind, fmt):
+    """Keys of large values, then of none (zeros; pages of no keys), then of
+    ordinary ones, all weights alike: the sums are the large ones'."""
+    b = Batch(seqs + IN_ONE, 2, G, 64, 16, fmt, kind)
+    run = np.arange(1536) // 512
+    x = b.g.uniform(0.5, 1.0, (1536, 2, 64))
+    values(b, 0, 2, x * np.array([2.0 ** power, 0.0, 1.0])[run][:, None, None])
+    b.pool.upload()
+    b.scale = 2.0 ** -30
+    tokens = [0, seqs[0][0] - 1]
+    check(b, b.run(causal=False), causal=False, tokens=tokens)
+    b.table[0, 32:64] = -1
+    check(b, b.run(causal=False), causal=False, hidden=np.nonzero(run == 1)[0], tokens=tokens)
+
+
+@pytest.mark.parametrize("fmt", ["fp4", "fp8"])
+@pytest.mark.parametrize("kind", WIDE)
+@pytest.mark.parametrize("power", [40, 100, 120])
+@pytest.mark.parametrize("seqs", [[(1, 1024)], [(2, 1024)], [(40, 1024)]])
+def test_heads_that_prefer_large_and_small_values(seqs, power, kind, fmt):
+    """Two heads of a group: the large values, which come first, are all of one's
+    result and have no weight, 2^-216, in the other's, which keeps its bits."""
+    b = Batch(seqs + IN_ONE, 2, 2, 64, 16, fmt, kind)
+    run = (np.arange(1024) // 512)[:, None, None]
+    values(b, 0, 0, np.where(run == 0, -4.0, 4.0) * np.ones((1024, 2, 64)))
+    values(b, 0, 2, b.g.standard_normal((1024, 2, 64)) * np.where(run == 0, 2.0 ** power, 1.0))
+    b.pool.upload()
+    b.q, b.held = put(np.broadcast_to(np.array([1.0, -1.0, 1.0, -1.0])[:, None], (b.T, 4, 64)), kind)
+    b.scale = 75 / 256
+    check(b, b.run(causal=False), causal=False, tokens=[0, seqs[0][0] - 1])
