@@ -19,8 +19,9 @@
 //            of p are of the unrounded ones, in fp32.
 // Keys that some rows see and others do not (a causal chunk's own, a window's
 // edge) are taken without a common reference, which a key that a row does not
-// see would give it: each key's own for its scores, and bf16 for its values,
-// with one bf16 weight more.
+// see would give it: each key's own for its scores, and bf16 for its values (times
+// 2^-8, so that the largest block is finite: nothing else keeps it from rows that do
+// not see it), with one bf16 weight more, which takes the sums' power.
 // A NaN block's scale is NaN and so are its products; a row of q that is not
 // finite has a NaN scale.
 #pragma once
@@ -252,6 +253,10 @@ __device__ __forceinline__ int reference(int before, int top) {
   const int now = max(top, kLastRef);
   return now > before || now + 8 < before ? now : before;
 }
+
+// Values without a reference may lie this far above that of the sums, which is raised
+// if they do not: a sum of them stays below 2^120.
+constexpr int kMixedShift = 8, kMixedReach = 60;
 
 // Under one reference a sum is below 2^60 (2^44 of weights, 2^16 of codes), but what
 // was summed under a higher one grows by the fall, up to 2^190 of it.  Where a row's

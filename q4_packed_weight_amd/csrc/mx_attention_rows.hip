@@ -321,7 +321,7 @@ __global__ __launch_bounds__(kWaves * 64, MIXED ? 1 : (kWavesPerSimd<NP, ND>)) v
   // keys that some rows see and others do not: no reference may come from a key
   // that a row does not see, and no NaN
   const auto compute_mixed = [&](int step) __attribute__((always_inline)) {
-    uint32_t rank[2];
+    uint32_t rank[2], v_top = 0;
     bool nan = false;
 #pragma unroll
     for (int j = 0; j < 2; j++) {
@@ -329,8 +329,9 @@ __global__ __launch_bounds__(kWaves * 64, MIXED ? 1 : (kWavesPerSimd<NP, ND>)) v
 #pragma unroll
       for (int p = 0; p < ND; p++) {
         rank[j] = max(rank[j], scale_rank(d.ks[j].of(p)));
+        v_top = max(v_top, scale_rank(d.vs[j].of(p)));
         nan |= has_nan<FMT>(d.v[j][p], d.vs[j].of(p));
-        const float s = block_scale(d.vs[j].of(p), 127 + X - v_ref);
+        const float s = block_scale(d.vs[j].of(p), -kMixedShift);
         uint8_t *const to = mem + (16 * j + r16) * VS + (64 * p + 16 * g) * 2;
         *reinterpret_cast<bf16x8 *>(to) = codes_operand_bf16<FMT>(&d.v[j][p][0], s);
         *reinterpret_cast<bf16x8 *>(to + 16) = codes_operand_bf16<FMT>(&d.v[j][p][W / 2], s);
@@ -363,13 +364,18 @@ __global__ __launch_bounds__(kWaves * 64, MIXED ? 1 : (kWavesPerSimd<NP, ND>)) v
         sees[4 * j + i] = see ? (_Float16)1.0f : (_Float16)0.0f;
       }
     }
-    const float less = raise(x, v_ref);
+    int v_new = v_ref;
+    if (__builtin_amdgcn_ballot_w64((int)v_top > v_ref + kMixedReach) != 0)
+      v_new = (int)wave_pk_max(v_top) - kMixedReach;
+    const float less = raise(x, v_new);
+    const float power = __builtin_ldexpf(1.0f, 127 + X + kMixedShift - v_ref);
     // as many bf16 as hold what fp16 holds of them in the other form
     bf16x8 p[NP + 1];
 #pragma unroll
     for (int i = 0; i < 8; i++) {
       float e = __builtin_amdgcn_exp2f(x[i] - less);
       l += e;
+      e *= power;
 #pragma unroll
       for (int n = 0; n <= NP; n++) {
         p[n][i] = (__bf16)e;

@@ -15,7 +15,8 @@ constexpr int kWaveKeys = kTile / kWaves;  // that a wave stages: 16, one step o
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // What a wave says of the 16 keys it has staged: a scale above its reference,
-// one at most 2^8 below it, a page that is none, a NaN value (mixed tiles).
+// one at most 2^8 below it, a page that is none; of mixed tiles a NaN value and,
+// in the byte above, the values' largest scale.
 enum : uint32_t { kOver = 1, kNearK = 2, kNearV = 4, kAbsent = 8, kNan = 16 };
 
 // A wave's share of a tile as it lies in memory: 16 codes (dims 16 n .. of lane
@@ -218,8 +219,9 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
         const int own = (int)max_of_key<LP>(scale_rank(d.ks[p]));
         k_base = 127 + X - own;
         nan |= has_nan<FMT>(d.v[p], d.vs[p]);
+        v_top = max(v_top, scale_rank(d.vs[p]));
         if (sub == 0) powers[b][n] = d.ok[p] ? __builtin_ldexpf(1.0f, own - X - 127) : -1.0f;
-        const float s = block_scale(d.vs[p], 0);
+        const float s = block_scale(d.vs[p], -kMixedShift);
         *reinterpret_cast<bf16x8 *>(v_to) = codes_operand_bf16<FMT>(&d.v[p][0], s);
         *reinterpret_cast<bf16x8 *>(v_to + 16) = codes_operand_bf16<FMT>(&d.v[p][W / 2], s);
       } else {
@@ -235,7 +237,7 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
     }
     uint32_t word = 0;
     if (mixed) {
-      if (__builtin_amdgcn_ballot_w64(nan) != 0) word = kNan;
+      word = wave_pk_max(v_top) << 8 | (__builtin_amdgcn_ballot_w64(nan) != 0 ? kNan : 0);
     } else {
       if (__builtin_amdgcn_ballot_w64((int)k_top > k_ref || (int)v_top > v_ref) != 0) word |= kOver;
       if (k_ref == kLastRef || __builtin_amdgcn_ballot_w64((int)k_top + 8 >= k_ref) != 0) word |= kNearK;
@@ -384,7 +386,7 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
         }
       }
     const float less = raise(mx);
-    const float f = __builtin_ldexpf(1.0f, 127 + X - v_ref);  // values are not scaled here
+    const float f = __builtin_ldexpf(1.0f, 127 + X + kMixedShift - v_ref);
 #pragma unroll
     for (int n = 0; n < kWaves; n++) {
       bf16x8 p[NP + 1];
@@ -469,18 +471,19 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
     const int b = t & 1, first = w.begin + t * kTile;
     bool mixed = is_mixed(t);
     uint32_t any;
-    {
+    int v_top;
+    const auto read = [&]() __attribute__((always_inline)) {
       const u32x4 words = *reinterpret_cast<const u32x4 *>(&staged[b][0]);
       any = (uint32_t)__builtin_amdgcn_readfirstlane((int)(words[0] | words[1] | words[2] | words[3]));
-    }
+      v_top = __builtin_amdgcn_readfirstlane((int)(max(max(words[0], words[1]), max(words[2], words[3])) >> 8));
+    };
+    read();
     if (!mixed && (any & (kOver | kNearK | kNearV | kAbsent)) != (kNearK | kNearV)) {
       mixed = (any & kAbsent) != 0;
       stage_again(t, mixed);
-      if (mixed) {
-        const u32x4 words = *reinterpret_cast<const u32x4 *>(&staged[b][0]);
-        any = (uint32_t)__builtin_amdgcn_readfirstlane((int)(words[0] | words[1] | words[2] | words[3]));
-      }
+      if (mixed) read();
     }
+    if (mixed && v_top > v_ref + kMixedReach) refer(v_top - kMixedReach);
     const bool sees = active && max(first, one.lo) <= min(first + kTile - 1, two.hi);
     bool there = true;
     for (int p = 0; p < (WHOLE ? 1 : PASSES); p++) there &= d.ok[p];

@@ -116,3 +116,57 @@ def test_heads_that_prefer_large_and_small_values(seqs, power, kind, fmt):
     b.q, b.held = put(np.broadcast_to(np.array([1.0, -1.0, 1.0, -1.0])[:, None], (b.T, 4, 64)), kind)
     b.scale = 75 / 256
     check(b, b.run(causal=False), causal=False, tokens=[0, seqs[0][0] - 1])
+
+
+CHUNKS = [([(4, 70)], 1), ([(4, 70)], 4), ([(2, 3000)], 4), ([(40, 200)], 2), ([(70, 1500)], 3)]
+
+
+@pytest.mark.parametrize("fmt", ["fp4", "fp8"])
+@pytest.mark.parametrize("kind", WIDE)
+@pytest.mark.parametrize("power", [20, 60, 112, 120])
+@pytest.mark.parametrize("others", [0.0, 1.0])
+@pytest.mark.parametrize("seqs,G", CHUNKS)
+def test_large_values_that_the_last_token_sees(seqs, G, others, power, kind, fmt):
+    """A chunk's last key has large values; all others ordinary ones, or zeros.
+    The tokens before it see nothing of them."""
+    b = Batch(seqs + (IN_ONE if others else []), 2, G, 64, 16, fmt, kind)
+    nq, nk = seqs[0]
+    x = b.g.standard_normal((nk, 2, 64)) * others
+    x[-1] = b.g.uniform(0.5, 1.0, (2, 64)) * 2.0 ** power
+    values(b, 0, 2, x)
+    b.pool.upload()
+    check(b, b.run(), tokens=sorted({0, nq // 2, nq - 2, nq - 1}))
+
+
+@pytest.mark.parametrize("fmt", ["fp4", "fp8"])
+@pytest.mark.parametrize("kind", WIDE)
+@pytest.mark.parametrize("power", [20, 60, 112, 120])
+@pytest.mark.parametrize("others", [[], IN_ONE], ids=["shares", "one"])
+@pytest.mark.parametrize("seqs,G", [([(4, 700)], 4), ([(2, 700)], 1), ([(40, 700)], 2)])
+def test_large_values_at_the_windows_edge(seqs, G, others, power, kind, fmt):
+    """The first key of the first token's window has large values: later tokens do
+    not see it, and keep the bits of all keys behind it."""
+    b = Batch(seqs + others, 2, G, 64, 16, fmt, kind)
+    nq, nk = seqs[0]
+    window = 500
+    x = b.g.standard_normal((nk, 2, 64))
+    x[nk - nq - window + 1] *= 2.0 ** power
+    values(b, 0, 2, x)
+    b.pool.upload()
+    check(b, b.run(window=window), window=window, tokens=sorted({0, 1, nq // 2, nq - 1}))
+
+
+@pytest.mark.parametrize("fmt", ["fp4", "fp8"])
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("seqs,G", CHUNKS)
+def test_blocks_beyond_fp32_where_only_the_last_token_looks(seqs, G, kind, fmt):
+    """The largest codes under the largest scale, 448 (6) times 2^127, are no value
+    of fp32; the tokens before the last have nothing to do with them."""
+    b = Batch(seqs, 2, G, 64, 16, fmt, kind)
+    nq, nk = seqs[0]
+    last = b.slots[0][-1:]
+    code = 0x7E if fmt == "fp8" else 0x77
+    b.pool.put(2, last, np.full((1, 2, b.pool.arrays[2].shape[-1]), code, np.uint8),
+               np.full((1, 2, 2), 254, np.uint8))
+    b.pool.upload()
+    check(b, b.run(), tokens=sorted({0, (nq - 1) // 2, nq - 2}))
