@@ -22,8 +22,10 @@
 // see would give it: each key's own for its scores, and bf16 for its values (times
 // 2^-8, so that the largest block is finite: nothing else keeps it from rows that do
 // not see it), with one bf16 weight more, which takes the sums' power.
+// The powers of q, k and scale are added as numbers before one of them is applied,
+// so that a score is what its product says also where its factors are not near 1.
 // A NaN block's scale is NaN and so are its products; a row of q that is not
-// finite has a NaN scale.
+// finite is all NaN.
 #pragma once
 
 #include "mx_common.h"
@@ -362,6 +364,12 @@ __device__ __forceinline__ bool has_nan(const uint32_t (&c)[W], uint32_t s) {
 #pragma unroll
     for (int i = 0; i < W; i++) r |= (((c[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
   return r;
+}
+
+// What a row's scores are multiplied by: 2^power of a.scale, and no infinity (0
+// times it is no score; others are beyond fp32 with it or without).
+__device__ __forceinline__ float score_scale(float scale, int power) {
+  return __builtin_ldexpf(scale, min(power, 127));
 }
 
 // Eight consecutive values of a row of q, as they lie in memory and in fp32: NP

@@ -46,7 +46,7 @@ __global__ __launch_bounds__(kWaves * 64, MIXED ? 1 : (kWavesPerSimd<NP, ND>)) v
   constexpr int kRegion = kStepKeys * VS > kRows * OS * 4 ? kStepKeys * VS : kRows * OS * 4;
   __shared__ __attribute__((aligned(16))) uint8_t lds[kWaves * kRegion];
   __shared__ float2 stats[kWaves][kRows];
-  __shared__ __attribute__((aligned(16))) float powers[kWaves][kStepKeys];
+  __shared__ __attribute__((aligned(16))) int powers[kWaves][kStepKeys];
   Work w;
   if (!work_of<kRows, kStepKeys>(a, blockIdx.x, w)) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
@@ -135,7 +135,7 @@ __global__ __launch_bounds__(kWaves * 64, MIXED ? 1 : (kWavesPerSimd<NP, ND>)) v
     load_pages(w.first + wave + kWaves, pages);
   }
   half8_t q[NP][ND][2];
-  float row_scale;
+  int row_power;
   {
     float f[ND][2][8];
     uint32_t amax = 0;
@@ -153,14 +153,14 @@ __global__ __launch_bounds__(kWaves * 64, MIXED ? 1 : (kWavesPerSimd<NP, ND>)) v
       }
     amax = swap_max_u32(amax);
     const int e = row_exponent(amax);
-    row_scale = amax >= 0x7F800000u ? __builtin_nanf("") : __builtin_ldexpf(a.scale, e);
+    row_power = e + a.scale_power;
 #pragma unroll
     for (int p = 0; p < ND; p++)
 #pragma unroll
       for (int h = 0; h < 2; h++)
 #pragma unroll
         for (int i = 0; i < 8; i++) {
-          const float v = __builtin_ldexpf(f[p][h][i], -e);
+          const float v = amax >= 0x7F800000u ? __builtin_nanf("") : __builtin_ldexpf(f[p][h][i], -e);
           q[0][p][h][i] = (_Float16)v;
           if constexpr (NP == 2) q[1][p][h][i] = (_Float16)(v - (float)q[0][p][h][i]);
         }
@@ -290,7 +290,7 @@ __global__ __launch_bounds__(kWaves * 64, MIXED ? 1 : (kWavesPerSimd<NP, ND>)) v
     const uint32_t ok = d.ok;
     load_step(step + kWaves, pages);
     load_pages(step + 2 * kWaves, pages);
-    const float c = __builtin_ldexpf(row_scale, k_ref - X - 127);
+    const float c = score_scale(a.scale, row_power + k_ref - X - 127);
     float x[8];
 #pragma unroll
     for (int i = 0; i < 8; i++) x[i] = s[i >> 2][i & 3] * c;
@@ -337,7 +337,7 @@ __global__ __launch_bounds__(kWaves * 64, MIXED ? 1 : (kWavesPerSimd<NP, ND>)) v
         *reinterpret_cast<bf16x8 *>(to + 16) = codes_operand_bf16<FMT>(&d.v[j][p][W / 2], s);
       }
       rank[j] = swap_max_u32(rank[j]);
-      if (g == 0) powers[wave][16 * j + r16] = __builtin_ldexpf(1.0f, (int)rank[j] - X - 127);
+      if (g == 0) powers[wave][16 * j + r16] = (int)rank[j] - X - 127;
     }
     __builtin_amdgcn_wave_barrier();
     float kf[2][ND];
@@ -355,12 +355,12 @@ __global__ __launch_bounds__(kWaves * 64, MIXED ? 1 : (kWavesPerSimd<NP, ND>)) v
     half8_t sees;
 #pragma unroll
     for (int j = 0; j < 2; j++) {
-      const f32x4 c = *reinterpret_cast<const f32x4 *>(&powers[wave][16 * j + 4 * g]);
+      const i32x4 c = *reinterpret_cast<const i32x4 *>(&powers[wave][16 * j + 4 * g]);
 #pragma unroll
       for (int i = 0; i < 4; i++) {
         const int n = 16 * j + 4 * g + i, key = first + n;
         const bool see = (ok >> n & 1) != 0 && key >= mine.lo && key <= mine.hi;
-        x[4 * j + i] = see ? s[j][i] * row_scale * c[i] : kMinusInf;
+        x[4 * j + i] = see ? __builtin_ldexpf(s[j][i] * a.scale, row_power + c[i]) : kMinusInf;
         sees[4 * j + i] = see ? (_Float16)1.0f : (_Float16)0.0f;
       }
     }

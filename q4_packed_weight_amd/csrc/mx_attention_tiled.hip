@@ -18,6 +18,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 // one at most 2^8 below it, a page that is none; of mixed tiles a NaN value and,
 // in the byte above, the values' largest scale.
 enum : uint32_t { kOver = 1, kNearK = 2, kNearV = 4, kAbsent = 8, kNan = 16 };
+constexpr int kNoKey = 0x7FFF;  // in place of a key's power
 
 // A wave's share of a tile as it lies in memory: 16 codes (dims 16 n .. of lane
 // n of a key's LP lanes) in each pass.
@@ -68,7 +69,7 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
   constexpr int LP = Data::LP, PASSES = Data::PASSES, W = Data::W;
   __shared__ __attribute__((aligned(16))) uint8_t k_lds[2][kTile * KS];
   __shared__ __attribute__((aligned(16))) uint8_t v_lds[2][kTile * VS];
-  __shared__ __attribute__((aligned(16))) float powers[2][kTile];
+  __shared__ __attribute__((aligned(16))) int powers[2][kTile];
   __shared__ __attribute__((aligned(16))) uint32_t staged[2][kWaves], tops[kWaves];
   Work w;
   if (!work_of<kRows, kTile>(a, blockIdx.x, w)) return;
@@ -86,7 +87,9 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
   const Range one = w.seq.sees(a, a.by_group.of(min(w.r0 + 32 * wave, last_row)));
   const Range two = w.seq.sees(a, a.by_group.of(min(w.r0 + 32 * wave + 31, last_row)));
   half8_t q[NP][DP / 16];
-  float row_scale;
+  int row_power;
+  // the largest x is the largest score: a negative scale's sign goes to q
+  const float scale = __builtin_fabsf(a.scale);
   {
     const int64_t at = (int64_t)(w.seq.q0 + token) * a.q_stride +
                        (int64_t)(w.kv_head * a.group + row - token * a.group) * D + 8 * half;
@@ -109,9 +112,8 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
     const uint32_t y0 = y[0], y1 = y[1];
     amax = max(y0, y1);
     const int e = row_exponent(amax);
-    // the largest x is the largest score: a negative scale's sign goes to q
-    const float sign = a.scale < 0.0f ? -1.0f : 1.0f;
-    row_scale = amax >= 0x7F800000u ? __builtin_nanf("") : __builtin_ldexpf(a.scale * sign, e);
+    const float sign = amax >= 0x7F800000u ? __builtin_nanf("") : a.scale < 0.0f ? -1.0f : 1.0f;
+    row_power = e + a.scale_power;
 #pragma unroll
     for (int s = 0; s < DP / 16; s++)
 #pragma unroll
@@ -220,7 +222,7 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
         k_base = 127 + X - own;
         nan |= has_nan<FMT>(d.v[p], d.vs[p]);
         v_top = max(v_top, scale_rank(d.vs[p]));
-        if (sub == 0) powers[b][n] = d.ok[p] ? __builtin_ldexpf(1.0f, own - X - 127) : -1.0f;
+        if (sub == 0) powers[b][n] = d.ok[p] ? own - X - 127 : kNoKey;
         const float s = block_scale(d.vs[p], -kMixedShift);
         *reinterpret_cast<bf16x8 *>(v_to) = codes_operand_bf16<FMT>(&d.v[p][0], s);
         *reinterpret_cast<bf16x8 *>(v_to + 16) = codes_operand_bf16<FMT>(&d.v[p][W / 2], s);
@@ -340,7 +342,7 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
     f32x16 s[2];
     scores(b, s);
     if constexpr (decltype(and_next)::value) stage_fast(b ^ 1);
-    const float c = __builtin_ldexpf(row_scale, k_ref - X - 127);
+    const float c = score_scale(scale, row_power + k_ref - X - 127);
     float mx = s[0][0];
 #pragma unroll
     for (int i = 1; i < 32; i++) mx = fmaxf(mx, s[i >> 4][i & 15]);
@@ -375,12 +377,12 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
 #pragma unroll
       for (int i = 0; i < 16; i += 4) {
         const int at = 32 * j + 2 * i + 4 * half;
-        const f32x4 c = *reinterpret_cast<const f32x4 *>(&powers[b][at]);
+        const i32x4 c = *reinterpret_cast<const i32x4 *>(&powers[b][at]);
 #pragma unroll
         for (int n = 0; n < 4; n++) {
           const int key = first + at + n;
-          const bool see = c[n] >= 0.0f && key >= mine.lo && key <= mine.hi;
-          s[j][i + n] = see ? s[j][i + n] * row_scale * c[n] : kMinusInf;
+          const bool see = c[n] != kNoKey && key >= mine.lo && key <= mine.hi;
+          s[j][i + n] = see ? __builtin_ldexpf(s[j][i + n] * scale, row_power + c[n]) : kMinusInf;
           sees |= (see ? 1u : 0u) << (16 * j + i + n);
           mx = fmaxf(mx, s[j][i + n]);
         }

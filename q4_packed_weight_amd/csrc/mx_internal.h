@@ -132,7 +132,8 @@ struct AttentionArgs {
   // their sequence by its sizes, and cut the keys into shares for about
   // shares_wanted (0: none) of them a key head; units they are at most
   int tiles, planned, shares_wanted, units;
-  float scale;         // times log2(e)
+  float scale;         // times log2(e), without its power of two: +-[0.5, 1), or 0
+  int scale_power;
   FastDiv by_page, by_group, by_kv_heads, by_tiles;
 };
 // Sizes alone decide the launch: the same call has the same workspace.

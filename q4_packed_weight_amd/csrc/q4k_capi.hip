@@ -852,7 +852,10 @@ int mx_attention(const void *q, int64_t q_stride, int type, const int32_t *query
   a.causal = causal != 0;
   // no sequence has more keys than 2^30: a longer window is none
   a.window = window > ((int64_t)1 << 30) ? 0 : (int)window;
-  a.scale = scale * 1.44269504088896340736f;
+  int power = 0, carry = 0;
+  a.scale = std::frexp(scale, &power);  // taken apart first: the product may pass fp32
+  a.scale = std::frexp(a.scale * 1.44269504088896340736f, &carry);
+  a.scale_power = power + carry;
   a.by_page = q4k::FastDiv((uint32_t)page_size);
   a.by_group = q4k::FastDiv((uint32_t)a.group);
   hipError_t e = q4k::mx_attention_launch(a, (hipStream_t)stream);

@@ -170,3 +170,54 @@ def test_blocks_beyond_fp32_where_only_the_last_token_looks(seqs, G, kind, fmt):
                np.full((1, 2, 2), 254, np.uint8))
     b.pool.upload()
     check(b, b.run(), tokens=sorted({0, (nq - 1) // 2, nq - 2}))
+
+
+SCORES = [([(1, 300)], 4), ([(3, 300)], 2), ([(40, 300)], 2)]
+
+
+@pytest.mark.parametrize("fmt", ["fp4", "fp8"])
+@pytest.mark.parametrize("kind", WIDE)
+@pytest.mark.parametrize("seqs,G", SCORES)
+def test_small_queries_of_large_keys(seqs, G, kind, fmt):
+    """Queries of 2^-124 and keys of 2^126: scores of some ones."""
+    b = Batch(seqs, 2, G, 64, 16, fmt, kind)
+    x = b.g.uniform(0.5, 1.0, (300, 2, 64)) * b.g.choice([-1, 1], (300, 2, 64))
+    values(b, 0, 0, x * 2.0 ** 126)
+    b.pool.upload()
+    q = b.g.uniform(0.5, 1.0, b.held.shape) * b.g.choice([-1, 1], b.held.shape)
+    b.q, b.held = put(q * 2.0 ** -124, kind)
+    b.scale = 0.25
+    check(b, b.run())
+
+
+@pytest.mark.parametrize("fmt", ["fp4", "fp8"])
+@pytest.mark.parametrize("kind", WIDE)
+@pytest.mark.parametrize("seqs,G", SCORES)
+def test_large_queries_across_large_keys(seqs, G, kind, fmt):
+    """Queries and keys of 2^100 in different dims: all scores are 0."""
+    b = Batch(seqs, 2, G, 64, 16, fmt, kind)
+    x = b.g.uniform(0.5, 1.0, (300, 2, 64)) * 2.0 ** 100
+    x[..., :32] = 0
+    values(b, 0, 0, x)
+    b.pool.upload()
+    q = b.g.uniform(0.5, 1.0, b.held.shape) * 2.0 ** 100
+    q[..., 32:] = 0
+    b.q, b.held = put(q, kind)
+    check(b, b.run())
+
+
+@pytest.mark.parametrize("fmt", ["fp4", "fp8"])
+@pytest.mark.parametrize("kind", WIDE)
+@pytest.mark.parametrize("scale,q,k", [(3e38, -75, -54), (-3e38, -75, -54), (2.0 ** -140, 70, 68)])
+@pytest.mark.parametrize("seqs,G", SCORES)
+def test_scales_near_fp32s_ends(seqs, G, scale, q, k, kind, fmt):
+    """Scales whose binary form, times log2(e), is past fp32's largest or below its
+    smallest normal, for queries and keys whose scores are some ones."""
+    b = Batch(seqs, 2, G, 64, 16, fmt, kind)
+    x = b.g.uniform(0.5, 1.0, (300, 2, 64)) * b.g.choice([-1, 1], (300, 2, 64))
+    values(b, 0, 0, x * 2.0 ** k)
+    b.pool.upload()
+    x = b.g.uniform(0.5, 1.0, b.held.shape) * b.g.choice([-1, 1], b.held.shape)
+    b.q, b.held = put(x * 2.0 ** q, kind)
+    b.scale = float(np.float32(scale))
+    check(b, b.run())
