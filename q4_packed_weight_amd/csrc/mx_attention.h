@@ -13,7 +13,7 @@
 //            still fits: exact for blocks whose scale lies up to 2^21 (MX_FP8) or
 //            2^36 (MX_FP4) below ref, as fp16's subnormals reach, and these
 //            operands keep them.
-//   weights  p = exp2(x - m + 10) with m the largest x so far or up to 4 less, so at
+//   weights  p = exp2(x - m), m 10 below the largest x so far or up to 4 less, so p at
 //            most 2^14: one fp16, off by 2^-11 of p, an eighth of what bf16 would
 //            leave of it; for fp32 a second one for what is left (2^-23).  The sums
 //            of p are of the unrounded ones, in fp32.
@@ -40,7 +40,12 @@ typedef short i16x2 __attribute__((ext_vector_type(2)));
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 
 constexpr float kMinusInf = -__builtin_inff();
-constexpr int kWeightExponent = 10;  // and up to 4 more
+// What the weights' exponents are counted from for a largest x of mx, and how far
+// above it x may come.  From 2^24 on fp32 has no such steps, and mx itself is taken.
+constexpr float kMostExponent = 14.0f;
+__device__ __forceinline__ float exponent_base(float mx) {
+  return __builtin_fabsf(mx) < 0x1p24f ? mx - 10.0f : mx;
+}
 // The power that the largest code takes within fp16: 448 * 2^6, 6 * 2^13.
 template <int FMT> constexpr int kCodeExponent = FMT == MX_FP8 ? 6 : 13;
 
@@ -411,7 +416,7 @@ __device__ __forceinline__ int row_exponent(uint32_t amax_bits) {
   return amax_bits == 0 ? 0 : (int)(amax_bits >> 23) - 127 - 14;
 }
 
-// The share of a partial result whose largest x is m in one whose is most.  A
+// The share of a partial result whose weights count from m in one whose do from most.  A
 // part without keys has m = -inf and zeros; one whose x are all NaN has m =
 // -inf and NaNs, which have to stay.
 __device__ __forceinline__ float part_share(float m, float most) {

@@ -208,9 +208,9 @@ __global__ __launch_bounds__(kWaves * 64, MIXED ? 1 : (kWavesPerSimd<NP, ND>)) v
 #pragma unroll
     for (int i = 1; i < 8; i++) mx = fmaxf(mx, x[i]);
     mx = swap_max32(swap_max16(mx));
-    const bool up = mx > m + 4.0f;
+    const bool up = mx - m > kMostExponent;
     if (__builtin_amdgcn_ballot_w64(up) != 0 || v_new != v_ref) {
-      const float f = up ? __builtin_amdgcn_exp2f(m - mx) : 1.0f;
+      const float to = up ? exponent_base(mx) : m, f = up ? __builtin_amdgcn_exp2f(m - to) : 1.0f;
       int power = v_ref - v_new, more = 0;
       if (power > 0) {
         uint32_t top = 0;
@@ -224,10 +224,10 @@ __global__ __launch_bounds__(kWaves * 64, MIXED ? 1 : (kWavesPerSimd<NP, ND>)) v
 #pragma unroll
       for (int i = 0; i < 16 * ND; i++)
         acc[i >> 2][i & 3] = __builtin_ldexpf(acc[i >> 2][i & 3] * f, power);
-      m = (up ? mx : m) + more;
+      m = to + more;
       v_ref = v_new;
     }
-    return (m == kMinusInf ? 0.0f : m) - kWeightExponent;
+    return m == kMinusInf ? 0.0f : m;
   };
 
   // Keys that all rows see (or none: absent ones).  The references stay as long
@@ -292,8 +292,11 @@ __global__ __launch_bounds__(kWaves * 64, MIXED ? 1 : (kWavesPerSimd<NP, ND>)) v
     load_pages(step + 2 * kWaves, pages);
     const float c = score_scale(a.scale, row_power + k_ref - X - 127);
     float x[8];
+    {  // rounded as its maximum is: no product with x - m
+#pragma clang fp contract(off)
 #pragma unroll
-    for (int i = 0; i < 8; i++) x[i] = s[i >> 2][i & 3] * c;
+      for (int i = 0; i < 8; i++) x[i] = s[i >> 2][i & 3] * c;
+    }
     if (ok != 0xFFFFFFFFu) {
 #pragma unroll
       for (int i = 0; i < 8; i++)

@@ -324,17 +324,17 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
   // as in the form for few rows: a maximum up to 2^4 too low stays
   const auto raise = [&](float mx) __attribute__((always_inline)) {
     mx = swap_max32(mx);
-    const bool up = mx > m + 4.0f;
+    const bool up = mx - m > kMostExponent;
     if (__builtin_amdgcn_ballot_w64(up) != 0) {
-      const float f = up ? __builtin_amdgcn_exp2f(m - mx) : 1.0f;
+      const float to = up ? exponent_base(mx) : m, f = up ? __builtin_amdgcn_exp2f(m - to) : 1.0f;
       l *= f;
 #pragma unroll
       for (int t = 0; t < 2 * ND; t++)
 #pragma unroll
         for (int i = 0; i < 16; i++) acc[t][i] *= f;
-      m = up ? mx : m;
+      m = to;
     }
-    return (m == kMinusInf ? 0.0f : m) - kWeightExponent;
+    return m == kMinusInf ? 0.0f : m;
   };
 
   // AND_NEXT: the next tile is staged among the scores' products
@@ -342,10 +342,19 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
     f32x16 s[2];
     scores(b, s);
     if constexpr (decltype(and_next)::value) stage_fast(b ^ 1);
-    const float c = score_scale(scale, row_power + k_ref - X - 127);
+    float c = score_scale(scale, row_power + k_ref - X - 127);
     float mx = s[0][0];
 #pragma unroll
     for (int i = 1; i < 32; i++) mx = fmaxf(mx, s[i >> 4][i & 15]);
+    // x - m by one rounding is off by what m was rounded by, which is no matter while it
+    // is a small part of one; beyond, both are rounded alike
+    if (__builtin_expect(__builtin_amdgcn_ballot_w64(__builtin_fabsf(mx * c) >= 0x1p23f) != 0, 0)) {
+#pragma clang fp contract(off)
+#pragma unroll
+      for (int i = 0; i < 32; i++) s[i >> 4][i & 15] *= c;
+      mx *= c;
+      c = 1.0f;
+    }
     const float less = raise(mx * c);
 #pragma unroll
     for (int n = 0; n < kWaves; n++) {

@@ -221,3 +221,26 @@ def test_scales_near_fp32s_ends(seqs, G, scale, q, k, kind, fmt):
     b.q, b.held = put(x * 2.0 ** q, kind)
     b.scale = float(np.float32(scale))
     check(b, b.run())
+
+
+@pytest.mark.parametrize("fmt", ["fp4", "fp8"])
+@pytest.mark.parametrize("kind", WIDE)
+@pytest.mark.parametrize("power", [66, 69, 70, 71, 72, 73, 74, 75, 80, 115])
+@pytest.mark.parametrize("seqs,G", SCORES)
+def test_large_scores(seqs, G, power, kind, fmt):
+    """Queries of 2^power and keys of 2^-50: scores about 2^(power - 46), at the upper
+    end 2^69, whose next neighbours in fp32 are some units and more apart: each token
+    takes the key of the largest."""
+    b = Batch(seqs, 2, G, 64, 16, fmt, kind)
+    nq, nk = seqs[0]
+    x = np.ones((nk, 2, 64))
+    x[7] = 1.5   # that all tokens see
+    x[-1] = 2.0  # that the last sees
+    values(b, 0, 0, x * 2.0 ** -50)
+    b.pool.upload()
+    b.q, b.held = put(np.full(b.held.shape, 2.0 ** power), kind)
+    y = host(b.run())[1:1 + nq].reshape(nq, 2, G, 64)
+    v = b.pool.values(2, b.slots[0])
+    want = np.where(np.arange(nq)[:, None, None] == nq - 1, v[-1], v[7])[:, :, None]
+    # one weight, its sum and their quotient: exact but for two fp32 roundings and y's own
+    assert (np.abs(y - want) <= rounding(kind, np.abs(want)) + 2 * U * np.abs(want)).all()
