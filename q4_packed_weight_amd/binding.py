@@ -521,8 +521,10 @@ def _rows(t, dtype, name, rows, heads, head_dim):
     width = heads * head_dim
     if t is None:
         return None, width
-    if (t.dtype is dtype and t.is_cuda and t.numel() == rows * width and t.is_contiguous()
-            and t.shape[0] == rows and t.get_device() == _current_device()):
+    shape = t.shape
+    if (t.dtype is dtype and t.is_cuda and t.is_contiguous() and rows > 0 and width > 0
+            and (shape == (rows, width) or shape == (rows, heads, head_dim))
+            and t.get_device() == _current_device()):
         return t.data_ptr(), width
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -530,7 +532,7 @@ def _rows(t, dtype, name, rows, heads, head_dim):
         raise ValueError(f"{name} must be a GPU tensor")
     if _current_device is not None and t.device.index != _current_device():
         raise ValueError(f"{name} is on {t.device}, the current device is another")
-    shape, stride = tuple(t.shape), t.stride()
+    stride = t.stride()
     if rows <= 0 or width <= 0:  # refused by the C side
         return t.data_ptr(), width
     if shape == (rows, width):
