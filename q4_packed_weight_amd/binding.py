@@ -514,7 +514,32 @@ def _choice(table, key, name):
     return code
 
 
-def _rows(t, dtype, name, rows, heads, head_dim):
+_device = torch.cuda.current_device if _current_device is None else _current_device
+
+
+def _here(t):
+    """The current device, not asked for where t needs none to be refused."""
+    return _device() if t.is_cuda else None
+
+
+def _elsewhere(t, name, here):
+    if t.get_device() != here:
+        raise ValueError(f"{name} is on {t.device}, the current device is another")
+
+
+def _local(t, dtype, name, need, here):
+    """_arg for a tensor that has to be on device `here`: pools, tables and positions
+    are read where the kernels run."""
+    if t is None:
+        return None
+    if not (t.dtype is dtype and t.is_contiguous() and t.get_device() == here
+            and t.numel() >= need):
+        _expect(t, dtype, name, need)
+        _elsewhere(t, name, here)
+    return t.data_ptr()
+
+
+def _rows(t, dtype, name, rows, heads, head_dim, here):
     """(pointer, values from a row to the next) of [rows][heads * head_dim] or
     [rows][heads][head_dim] values; rows may lie apart, as slices of a wider
     matrix do."""
@@ -522,16 +547,14 @@ def _rows(t, dtype, name, rows, heads, head_dim):
     if t is None:
         return None, width
     shape = t.shape
-    if (t.dtype is dtype and t.is_cuda and t.is_contiguous() and rows > 0 and width > 0
-            and (shape == (rows, width) or shape == (rows, heads, head_dim))
-            and t.get_device() == _current_device()):
+    if (t.dtype is dtype and t.get_device() == here and t.is_contiguous() and rows > 0 and width > 0
+            and (shape == (rows, width) or shape == (rows, heads, head_dim))):
         return t.data_ptr(), width
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
-    if _current_device is not None and t.device.index != _current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is another")
+    _elsewhere(t, name, here)
     stride = t.stride()
     if rows <= 0 or width <= 0:  # refused by the C side
         return t.data_ptr(), width
@@ -551,11 +574,11 @@ def mx_rotary(x, positions, frequencies, amplitude, n_tokens, n_heads, head_dim,
               layout, y, stream=None):
     """Rotary positions; layout is "half" or "interleaved", y may be x."""
     T, H, D, R = int(n_tokens), int(n_heads), int(head_dim), int(rotary_dim)
-    t, lay = _mx_type(x, "x"), _choice(ROTARY_LAYOUT, layout, "layout")
-    xp, xs = _rows(x, x.dtype, "x", T, H, D)
-    yp, ys = _rows(y, x.dtype, "y", T, H, D)
-    rc = lib().mx_rotary(xp, xs, t, _arg(positions, torch.int64, "positions", max(T, 0)),
-                         _arg(frequencies, torch.float64, "frequencies", max(R // 2, 0)),
+    t, here, lay = _mx_type(x, "x"), _here(x), _choice(ROTARY_LAYOUT, layout, "layout")
+    xp, xs = _rows(x, x.dtype, "x", T, H, D, here)
+    yp, ys = _rows(y, x.dtype, "y", T, H, D, here)
+    rc = lib().mx_rotary(xp, xs, t, _local(positions, torch.int64, "positions", max(T, 0), here),
+                         _local(frequencies, torch.float64, "frequencies", max(R // 2, 0), here),
                          float(amplitude), T, H, D, R, lay, yp, ys, _stream(stream))
     _check(rc, "mx_rotary")
     return y
@@ -575,9 +598,9 @@ def mx_rotary_frequencies(rotary_dim, base=10000.0, scaling="none", factor=1.0, 
     return f, amplitude.value
 
 
-def _pool(k_codes, k_scales, v_codes, v_scales, n_pages, page_size, heads, head_dim, f):
+def _pool(k_codes, k_scales, v_codes, v_scales, n_pages, page_size, heads, head_dim, f, here):
     n = _mx_need(n_pages * heads * page_size, head_dim) if heads > 0 and page_size > 0 else 0
-    return [_arg(t, torch.uint8, name, need) for t, name, need in (
+    return [_local(t, torch.uint8, name, need, here) for t, name, need in (
         (k_codes, "k_codes", n * f // 8), (k_scales, "k_scales", n // 32),
         (v_codes, "v_codes", n * f // 8), (v_scales, "v_scales", n // 32))]
 
@@ -586,12 +609,13 @@ def mx_cache_write(k, v, slots, n_tokens, n_heads, head_dim, fmt, k_codes, k_sca
                    v_scales, n_pages, page_size, stream=None):
     """Rows of keys and values to the blocks of their slots; -1 leaves a token out."""
     T, H, D, N, B = int(n_tokens), int(n_heads), int(head_dim), int(n_pages), int(page_size)
-    t, f = _mx_type(k, "k"), _mx_format(fmt)
-    kp, ks = _rows(k, k.dtype, "k", T, H, D)
-    vp, vs = _rows(v, k.dtype, "v", T, H, D)
-    rc = lib().mx_cache_write(kp, ks, vp, vs, t, _arg(slots, torch.int64, "slots", max(T, 0)), T, H,
-                              D, f, *_pool(k_codes, k_scales, v_codes, v_scales, N, B, H, D, f), N,
-                              B, _stream(stream))
+    t, f, here = _mx_type(k, "k"), _mx_format(fmt), _here(k)
+    kp, ks = _rows(k, k.dtype, "k", T, H, D, here)
+    vp, vs = _rows(v, k.dtype, "v", T, H, D, here)
+    pool = _pool(k_codes, k_scales, v_codes, v_scales, N, B, H, D, f, here)
+    rc = lib().mx_cache_write(kp, ks, vp, vs, t,
+                              _local(slots, torch.int64, "slots", max(T, 0), here), T, H, D, f,
+                              *pool, N, B, _stream(stream))
     _check(rc, "mx_cache_write")
 
 
@@ -599,12 +623,12 @@ def mx_cache_read(slots, n_tokens, n_heads, head_dim, fmt, k_codes, k_scales, v_
                   n_pages, page_size, k, v, stream=None):
     """The values of slots, rounded to k's and v's type; -1 reads as zeros."""
     T, H, D, N, B = int(n_tokens), int(n_heads), int(head_dim), int(n_pages), int(page_size)
-    t, f = _mx_type(k, "k"), _mx_format(fmt)
-    kp, ks = _rows(k, k.dtype, "k", T, H, D)
-    vp, vs = _rows(v, k.dtype, "v", T, H, D)
-    rc = lib().mx_cache_read(_arg(slots, torch.int64, "slots", max(T, 0)), T, H, D, f,
-                             *_pool(k_codes, k_scales, v_codes, v_scales, N, B, H, D, f), N, B, kp,
-                             ks, vp, vs, t, _stream(stream))
+    t, f, here = _mx_type(k, "k"), _mx_format(fmt), _here(k)
+    kp, ks = _rows(k, k.dtype, "k", T, H, D, here)
+    vp, vs = _rows(v, k.dtype, "v", T, H, D, here)
+    pool = _pool(k_codes, k_scales, v_codes, v_scales, N, B, H, D, f, here)
+    rc = lib().mx_cache_read(_local(slots, torch.int64, "slots", max(T, 0), here), T, H, D, f,
+                             *pool, N, B, kp, ks, vp, vs, t, _stream(stream))
     _check(rc, "mx_cache_read")
     return k, v
 
@@ -626,15 +650,17 @@ def mx_attention(q, query_starts, key_counts, pages, n_tokens, n_heads, n_kv_hea
     workspace may be None where mx_attention_workspace_size gives 0."""
     T, H, HK, D = int(n_tokens), int(n_heads), int(n_kv_heads), int(head_dim)
     S, P, N, B = int(n_seqs), int(pages_per_seq), int(n_pages), int(page_size)
-    t, f, i32 = _mx_type(q, "q"), _mx_format(fmt), torch.int32
-    qp, qs = _rows(q, q.dtype, "q", T, H, D)
-    yp, ys = _rows(y, q.dtype, "y", T, H, D)
-    rc = lib().mx_attention(qp, qs, t, _arg(query_starts, i32, "query_starts", max(S + 1, 0)),
-                            _arg(key_counts, i32, "key_counts", max(S, 0)),
-                            _arg(pages, i32, "pages", max(S, 0) * max(P, 0)), T, H, HK, D, S, P,
-                            int(max_queries), float(scale), int(bool(causal)), int(window), f,
-                            *_pool(k_codes, k_scales, v_codes, v_scales, N, B, HK, D, f), N, B, yp,
-                            ys, _arg(workspace, torch.uint8, "workspace", 0),
+    t, f, i32, here = _mx_type(q, "q"), _mx_format(fmt), torch.int32, _here(q)
+    qp, qs = _rows(q, q.dtype, "q", T, H, D, here)
+    yp, ys = _rows(y, q.dtype, "y", T, H, D, here)
+    pool = _pool(k_codes, k_scales, v_codes, v_scales, N, B, HK, D, f, here)
+    rc = lib().mx_attention(qp, qs, t,
+                            _local(query_starts, i32, "query_starts", max(S + 1, 0), here),
+                            _local(key_counts, i32, "key_counts", max(S, 0), here),
+                            _local(pages, i32, "pages", max(S, 0) * max(P, 0), here), T, H, HK, D,
+                            S, P, int(max_queries), float(scale), int(bool(causal)), int(window),
+                            f, *pool, N, B, yp, ys,
+                            _local(workspace, torch.uint8, "workspace", 0, here),
                             0 if workspace is None else workspace.numel(), _stream(stream))
     _check(rc, "mx_attention")
     return y

@@ -21,11 +21,11 @@ class Tensor:
 
 @pytest.fixture(autouse=True)
 def device(monkeypatch):
-    monkeypatch.setattr(binding, "_current_device", lambda: 0)
+    monkeypatch.setattr(binding, "_device", lambda: 0)
 
 
 def rows(t, n, heads, head_dim):
-    return binding._rows(Tensor(t), torch.float32, "x", n, heads, head_dim)
+    return binding._rows(Tensor(t), torch.float32, "x", n, heads, head_dim, 0)
 
 
 def test_rows_of_both_shapes_and_strides():
@@ -49,3 +49,33 @@ def test_rows_that_do_not_lie_together_are_refused():
     for t in (x[..., :32], x.transpose(1, 2)[:, :32], x[..., ::2], x.transpose(0, 1)[:4, :4].transpose(1, 2)):
         with pytest.raises(ValueError):
             rows(t, 4, t.shape[1], t.shape[2])
+
+
+CALLS = {
+    "mx_rotary": lambda f, i: binding.mx_rotary(f[0], i[0], f[1], 1.0, 2, 2, 32, 32, "half", f[0]),
+    "mx_cache_write": lambda f, i: binding.mx_cache_write(f[0], f[0], i[0], 2, 2, 32, "fp8", *f[2:6], 4, 16),
+    "mx_cache_read": lambda f, i: binding.mx_cache_read(i[0], 2, 2, 32, "fp8", *f[2:6], 4, 16, f[0], f[0]),
+    "mx_attention": lambda f, i: binding.mx_attention(f[0], *i[1:4], 2, 2, 2, 32, 2, 2, 1, 1.0, True, 0, "fp8",
+                                                      *f[2:6], 4, 16, f[0], f[6])}
+USES = {"mx_rotary": ([0, 1], [0]), "mx_cache_write": ([0, 2, 3, 4, 5], [0]),
+        "mx_cache_read": ([0, 2, 3, 4, 5], [0]), "mx_attention": ([0, 2, 3, 4, 5, 6], [1, 2, 3])}
+
+
+@pytest.mark.parametrize("call,place", [(c, (k, n)) for c, u in USES.items() for k in (0, 1) for n in u[k]])
+def test_tensors_of_another_device_are_refused(monkeypatch, call, place):
+    """Each of them: nothing is launched."""
+    def never(*a):
+        raise AssertionError("launched")
+    monkeypatch.setattr(binding, "_stream", lambda s: 0)
+    lib = type("Lib", (), {call: never})
+    monkeypatch.setattr(binding, "lib", lambda: lib)
+    u8 = torch.zeros(4 * 2 * 16 * 32, dtype=torch.uint8)
+
+    def tensors(other):
+        f = [torch.zeros(2, 64), torch.zeros(16, dtype=torch.float64), u8, u8, u8, u8, u8]
+        i = [torch.zeros(4, dtype=torch.int64)] + [torch.zeros(4, dtype=torch.int32)] * 3
+        return [[Tensor(t, int(other == (k, n))) for n, t in enumerate(g)] for k, g in enumerate((f, i))]
+    with pytest.raises(AssertionError, match="launched"):  # all on the current one
+        CALLS[call](*tensors(None))
+    with pytest.raises(ValueError, match="current device is another"):
+        CALLS[call](*tensors(place))
