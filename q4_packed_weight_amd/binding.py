@@ -585,9 +585,12 @@ def mx_rotary(x, positions, frequencies, amplitude, n_tokens, n_heads, head_dim,
 
 
 def mx_rotary_frequencies(rotary_dim, base=10000.0, scaling="none", factor=1.0, trained=8192.0,
-                          low=1.0, high=32.0):
+                          low=1.0, high=None):
     """(fp64 tensor on the host of rotary_dim / 2 frequencies, amplitude); the
-    scaling is "none", "linear", "ntk", "yarn" or "bands"."""
+    scaling is "none", "linear", "ntk", "yarn" or "bands".  Without `high` bands end
+    at 4 turns and YaRN's ramp at 32, as models trained with them have it."""
+    if high is None:
+        high = 4.0 if scaling == "bands" else 32.0
     n = int(rotary_dim)
     f = torch.zeros(max(n // 2, 1), dtype=torch.float64)
     amplitude = ctypes.c_double(1.0)

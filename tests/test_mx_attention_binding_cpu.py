@@ -79,3 +79,20 @@ def test_tensors_of_another_device_are_refused(monkeypatch, call, place):
         CALLS[call](*tensors(None))
     with pytest.raises(ValueError, match="current device is another"):
         CALLS[call](*tensors(place))
+
+
+def test_bands_and_yarn_have_their_own_defaults():
+    """Bands lie between 1 turn over the trained positions and 4, YaRN's ramp between
+    1 and 32; given ones are taken by both."""
+    for scaling, high in (("bands", 4.0), ("yarn", 32.0)):
+        f, _ = binding.mx_rotary_frequencies(128, 500000.0, scaling, 8.0)
+        want, _ = binding.mx_rotary_frequencies(128, 500000.0, scaling, 8.0, 8192.0, 1.0, high)
+        assert torch.equal(f, want)
+        other, _ = binding.mx_rotary_frequencies(128, 500000.0, scaling, 8.0, high=9.0)
+        assert not torch.equal(f, other)
+    # turns over 8192 positions: 4 and more are kept, 1 and less are divided
+    f, _ = binding.mx_rotary_frequencies(128, 500000.0, "bands", 8.0)
+    plain, _ = binding.mx_rotary_frequencies(128, 500000.0)
+    turns = 8192 * plain / 6.283185307179586
+    assert torch.equal(f[turns >= 4], plain[turns >= 4])
+    assert torch.allclose(f[turns <= 1], plain[turns <= 1] / 8, rtol=1e-15, atol=0)
