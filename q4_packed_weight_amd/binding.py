@@ -592,7 +592,8 @@ def mx_rotary_frequencies(rotary_dim, base=10000.0, scaling="none", factor=1.0, 
     if high is None:
         high = 4.0 if scaling == "bands" else 32.0
     n = int(rotary_dim)
-    f = torch.zeros(max(n // 2, 1), dtype=torch.float64)
+    # a size that the C side refuses gets no table
+    f = torch.zeros(n // 2 if 0 < n <= 512 else 0, dtype=torch.float64)
     amplitude = ctypes.c_double(1.0)
     rc = lib().mx_rotary_frequencies(n, float(base), _choice(ROTARY_SCALING, scaling, "scaling"),
                                      float(factor), float(trained), float(low), float(high),

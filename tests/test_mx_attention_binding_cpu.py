@@ -96,3 +96,10 @@ def test_bands_and_yarn_have_their_own_defaults():
     turns = 8192 * plain / 6.283185307179586
     assert torch.equal(f[turns >= 4], plain[turns >= 4])
     assert torch.allclose(f[turns <= 1], plain[turns <= 1] / 8, rtol=1e-15, atol=0)
+
+
+@pytest.mark.parametrize("d", [514, 1 << 45, 1 << 62, -2, 0, 7])
+def test_sizes_of_no_table_are_refused_without_one(d):
+    with pytest.raises(binding.Q4KError) as e:
+        binding.mx_rotary_frequencies(d)
+    assert e.value.code == binding.Q4K_EINVAL_DIM
