@@ -288,14 +288,22 @@ int mx_cache_read(const int64_t *slots, int64_t n_tokens, int64_t n_heads, int64
  *              undefined.  Calls that share one must not overlap in time.
  * What lies between q and y (fp16 operands with powers of two taken out, fp32
  * sums):
- *   q          exact for bf16 and fp16; fp32 as two fp16 values, off by 2^-23
- *              of each; below 2^-29 of a row's largest bits are lost
+ *   q          off by up to 2^-39 of a row's largest value (nothing, for bf16
+ *              and fp16, above 2^-28 of it); fp32, as two fp16 values, also
+ *              by 2^-23 of each
  *   k, v       exact where the scale bytes of the keys taken together (32 or
  *              64 in a row) lie within 13 (MX_FP8) or 28 (MX_FP4) of their
  *              largest and that above 2^-55; lower blocks lose bits, from the
- *              lowest on
- *   w          off by 2^-11 of each (bf16 and fp16), 2^-23 (fp32)
+ *              lowest on: up to 2^-31 of the largest value there, or 2^-94
+ *   w          off by 2^-11 of each (bf16 and fp16), 2^-23 (fp32), and by up to
+ *              2^-35 of the row's largest; by more where values of one row lie
+ *              more than 2^65 apart
+ * Values may be any finite ones of fp32, and y is finite then.  Scores, scale *
+ * q . k, have to lie within 2^126 of 0 (beyond, y may be NaN or zeros); where
+ * they pass 2^24 and values lie 2^65 apart as well, weights are not kept.
  * The order of the sums depends on the sizes, starts and counts alone.
+ * A sequence's keys are walked by many workgroups at once only in batches of at
+ * most 512 sequences that do not fill the chip without it.
  */
 int64_t mx_attention_workspace_size(int64_t n_tokens, int64_t n_heads, int64_t n_kv_heads,
                                     int64_t head_dim, int64_t n_seqs, int64_t pages_per_seq,

@@ -6,8 +6,9 @@
 //   queries  q = 2^e (h + l): e by row, so that the row's largest value lies in
 //            [2^14, 2^15); h alone holds bf16 and fp16 values, of fp32 h is
 //            rounded to fp16 and l what is left, rounded too (off by 2^-23 of
-//            the value).  What lies 2^-29 below the row's
-//            largest is lost bit by bit.
+//            the value).  Both end at fp16's smallest step, 2^-24: off by 2^-39 of
+//            the row's largest, which bf16 and fp16 values notice from 2^-28 of it
+//            down, and the l of fp32 from 2^-16.
 //   keys and values  code * 2^(s - ref), ref the largest scale byte among the
 //            keys taken together or up to 8 above it, so that the largest code
 //            still fits: exact for blocks whose scale lies up to 2^21 (MX_FP8) or
@@ -15,8 +16,9 @@
 //            operands keep them.
 //   weights  p = exp2(x - m), m 10 below the largest x so far or up to 4 less, so p at
 //            most 2^14: one fp16, off by 2^-11 of p, an eighth of what bf16 would
-//            leave of it; for fp32 a second one for what is left (2^-23).  The sums
-//            of p are of the unrounded ones, in fp32.
+//            leave of it; for fp32 a second one for what is left (2^-23); as fp16's
+//            steps end, either by 2^-25 as well, 2^-35 of the largest, and below that
+//            p is 0.  The sums of p are of the unrounded ones, in fp32.
 // Keys that some rows see and others do not (a causal chunk's own, a window's
 // edge) are taken without a common reference, which a key that a row does not
 // see would give it: each key's own for its scores, and bf16 for its values (times
@@ -112,8 +114,10 @@ struct Work {
 // The sequences' units lie one after the other: a sequence of `tiles` tiles whose
 // keys make `shares` shares at most has tiles * shares.  The shares' length is one
 // for the whole batch, so that about a.shares_wanted workgroups come out and none
-// works longer than the others.  Every wave finds its place for itself, 64
-// sequences at a time.  BY_TILE: `n` counts tiles, not units.
+// works longer than that; a tile's last share is what is left, often much less, and
+// a window's tiles see fewer keys (their own tokens') than are counted here (those of
+// max_queries).  Every wave finds its place for itself, 64 sequences at a time.
+// BY_TILE: `n` counts tiles, not units.
 template <int ROWS, int KEYS, bool BY_TILE>
 __device__ __forceinline__ bool find_work(const AttentionArgs &a, uint32_t n, Work &w, int &tile,
                                           int &share) {

@@ -34,8 +34,8 @@ constexpr int kWavesPerSimd = ND == 1 ? 5 : ND == 2 ? (NP == 1 ? 4 : 3) : ND == 
 // and in LDS, the next one's are sent for, and its weights and sums are made
 // while they come.  The four results, and those of the shares, are joined by
 // their largest x.  Bound by memory and, for small batches, by its latency: 64
-// tokens over 1024 .. 8192 keys of 8 heads of 128 (MX_FP8, 621 MB) 150 us, 4.1 TB/s;
-// 2 tokens over 131072 keys in MX_FP4 (213 MB) 56 us; one over 1000 keys 10.5 us, of
+// tokens over 1024 .. 8192 keys of 8 heads of 128 (MX_FP8, 621 MB) 140 us, 4.4 TB/s;
+// 2 tokens over 131072 keys in MX_FP4 (213 MB) 55 us; one over 1000 keys 10.5 us, of
 // which the join is 4: starts, pages and codes are three loads that wait for one
 // another, and a step alone on its SIMD takes 1.5 us.
 template <int NP, int FMT, int ND, bool MIXED, bool FOURS>
@@ -527,7 +527,9 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a) {
   }
 }
 
-// More than one tile of 16 rows: the form for many rows.
+// More than one tile of 16 rows: the form for many rows.  64 tokens over 4096 keys of
+// 4 heads of 128 (MX_FP8, 280 MB): 70 us with 8 rows a head, 154 with 32 here, of
+// which three quarters of a 128-row tile are idle.
 bool tiled(const AttentionArgs &a) { return (int64_t)a.max_queries * a.group > kRows; }
 
 // Workgroups on the chip at a time.
@@ -555,7 +557,10 @@ constexpr int kMaxPlanned = 512;  // sequences that every workgroup looks throug
 
 // Tiles are laid out by the sequences' own sizes where those are few enough to
 // look through; keys are cut into shares where the tiles alone are fewer than
-// twice (many rows: once) the workgroups that run at a time.
+// twice (many rows: once) the workgroups that run at a time.  With more tiles, or
+// more sequences, each tile's keys are one workgroup's: of 256 tokens with 8 heads, one
+// over 131072 keys and the others over 500, that one takes 1.2 ms (of 200, cut, all
+// take 0.11); 500 and 600 over 500 to 600 keys each take 117 and 133 us, 5.2 TB/s.
 int64_t mx_attention_workspace_bytes(AttentionArgs &a) {
   const int rows = tiled(a) ? kTiledRows : kRows, keys = tiled(a) ? kTiledKeys : kStepKeys;
   a.tiles = (int)(((int64_t)a.max_queries * a.group + rows - 1) / rows);

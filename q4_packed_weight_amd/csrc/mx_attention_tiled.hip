@@ -54,10 +54,11 @@ template <int LP> __device__ __forceinline__ uint32_t max_of_key(uint32_t v) {
 // The tile's references are those of the tiles before as long as they hold (stage
 // says so, stage_again mends it), so that nothing is exchanged before the barrier.
 // Bound by the waits of two waves a SIMD: of 2048 tokens over 8192 keys (32 heads of
-// 128, 241 GFLOP, 322 us, 0.75 PFLOP/s, half of a large fp16 product's rate) the
-// matrix pipe works 28% and the vector unit 43% of the time.  Tried: operands read
-// ahead in a fixed order, with the sums kept in memory around that loop so that its
-// registers suffice 361 us, without 390; 2 x 32-key halves 477.
+// 128, 241 GFLOP, 329 to 340 us by the card, 0.73 PFLOP/s, half of a large fp16
+// product's rate) the matrix pipe works 28% and the vector unit 44% of the time.
+// Tried, when it took 322: operands read ahead in a fixed order, with the sums kept in
+// memory around that loop so that its registers suffice 361 us, without 390; 2 x 32-key
+// halves 477.
 // WHOLE: pages of a multiple of 16 keys, so that a wave's 16 lie in one and
 // their addresses are scalars (351 against 341 us when it came).
 template <int NP, int FMT, int ND, bool WHOLE>
