@@ -271,11 +271,11 @@ constexpr int kMixedShift = 8, kMixedReach = 60;
 
 // Under one reference a sum is below 2^60 (2^44 of weights, 2^16 of codes), but what
 // was summed under a higher one grows by the fall, up to 2^190 of it.  Where a row's
-// largest sum, of magnitude bits `top`, would pass 2^126, its maximum is taken to be
-// higher by this power of two, and sums and sum of weights are made smaller by it:
-// its weights from there on are smaller too, and count for less than 2^-65 of what
+// largest sum, of magnitude bits `top`, would pass 2^126, this power of two is held
+// back: sums and sum of weights are smaller by it, and so are the weights until the
+// reference or the maximum changes again, which count for less than 2^-65 of what
 // there is.
-__device__ __forceinline__ int excess(uint32_t top, int fall) {
+__device__ __forceinline__ int held_back(uint32_t top, int fall) {
   return max(0, (int)(top >> 23) + fall - 252);
 }
 // A sum's magnitude bits; what is not finite stays so, and holds nothing back.

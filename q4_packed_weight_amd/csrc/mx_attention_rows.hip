@@ -170,6 +170,7 @@ __global__ __launch_bounds__(kWaves * 64, MIXED ? 1 : (kWavesPerSimd<NP, ND>)) v
 #pragma unroll
   for (int i = 0; i < 4 * ND; i++) acc[i] = f32x4{0, 0, 0, 0};
   float m = kMinusInf, l = 0.0f;
+  bool any_held = false;  // then stats has rows' m without and what is held back
   int v_ref = kFirstRef;
   uint8_t *const mem = lds + wave * kRegion;
   typedef __attribute__((address_space(3))) s16x4 LdsS16x4;
@@ -208,24 +209,31 @@ __global__ __launch_bounds__(kWaves * 64, MIXED ? 1 : (kWavesPerSimd<NP, ND>)) v
 #pragma unroll
     for (int i = 1; i < 8; i++) mx = fmaxf(mx, x[i]);
     mx = swap_max32(swap_max16(mx));
-    const bool up = mx - m > kMostExponent;
-    if (__builtin_amdgcn_ballot_w64(up) != 0 || v_new != v_ref) {
-      const float to = up ? exponent_base(mx) : m, f = up ? __builtin_amdgcn_exp2f(m - to) : 1.0f;
-      int power = v_ref - v_new, more = 0;
-      if (power > 0) {
+    if (__builtin_amdgcn_ballot_w64(mx - m > kMostExponent) != 0 || v_new != v_ref) {
+      int power = v_ref - v_new;
+      if (power > 0 || (power < 0 && any_held)) {
+        float2 kept = make_float2(m, 0.0f);
+        if (any_held) kept = stats[wave][r16];
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < 16 * ND; i++) top = max(top, sum_bits(acc[i >> 2][i & 3]));
-        const float most = __builtin_bit_cast(float, swap_max_u32(top)) * f;
-        more = excess(__builtin_bit_cast(uint32_t, most), power);
+        power += (int)kept.y;
+        const int more = held_back(swap_max_u32(top), power);
         power -= more;
+        l = __builtin_ldexpf(l, (int)kept.y - more);
+        m = kept.x + more;
+        any_held = __builtin_amdgcn_ballot_w64(more != 0) != 0;
+        if (any_held) stats[wave][r16] = make_float2(kept.x, more);
       }
-      l = __builtin_ldexpf(l * f, -more);
+      v_ref = v_new;
+      const bool up = mx - m > kMostExponent;
+      const float to = up ? exponent_base(mx) : m, f = up ? __builtin_amdgcn_exp2f(m - to) : 1.0f;
+      l *= f;
 #pragma unroll
       for (int i = 0; i < 16 * ND; i++)
         acc[i >> 2][i & 3] = __builtin_ldexpf(acc[i >> 2][i & 3] * f, power);
-      m = to + more;
-      v_ref = v_new;
+      m = to;
+      if (any_held && up) stats[wave][r16] = make_float2(m, 0.0f);
     }
     return m == kMinusInf ? 0.0f : m;
   };

@@ -72,6 +72,7 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
   __shared__ __attribute__((aligned(16))) uint8_t v_lds[2][kTile * VS];
   __shared__ __attribute__((aligned(16))) int powers[2][kTile];
   __shared__ __attribute__((aligned(16))) uint32_t staged[2][kWaves], tops[kWaves];
+  __shared__ float2 held[kWaves][32];  // where any_held: rows' m without what is held back, and that
   Work w;
   if (!work_of<kRows, kTile>(a, blockIdx.x, w)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -280,6 +281,7 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
 #pragma unroll
     for (int i = 0; i < 16; i++) acc[t][i] = 0.0f;
   float m = kMinusInf, l = 0.0f;
+  bool any_held = false;
   typedef __attribute__((address_space(3))) s16x4 LdsS16x4;
   const int v_at = (4 * half + (lane >> 2 & 3)) * VS + 32 * (lane >> 4 & 1) + 8 * (lane & 3);
   const int k_at = r32 * KS + 16 * half;
@@ -307,16 +309,21 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
   // what was summed to the values' new reference
   const auto refer = [&](int v_new) __attribute__((always_inline)) {
     int power = v_ref - v_new;
-    if (power > 0) {
+    if (power > 0 || any_held) {
+      float2 kept = make_float2(m, 0.0f);
+      if (any_held) kept = held[wave][r32];
       uint32_t top = 0;
 #pragma unroll
       for (int i = 0; i < 32 * ND; i++) top = max(top, sum_bits(acc[i >> 4][i & 15]));
       const auto y = __builtin_amdgcn_permlane32_swap(top, top, false, false);
       const uint32_t y0 = y[0], y1 = y[1];
-      const int more = excess(max(y0, y1), power);
-      m += more;
-      l = __builtin_ldexpf(l, -more);
+      power += (int)kept.y;
+      const int more = held_back(max(y0, y1), power);
       power -= more;
+      l = __builtin_ldexpf(l, (int)kept.y - more);
+      m = kept.x + more;
+      any_held = __builtin_amdgcn_ballot_w64(more != 0) != 0;
+      if (any_held) held[wave][r32] = make_float2(kept.x, more);
     }
 #pragma unroll
     for (int i = 0; i < 32 * ND; i++) acc[i >> 4][i & 15] = __builtin_ldexpf(acc[i >> 4][i & 15], power);
@@ -334,6 +341,7 @@ __global__ __launch_bounds__(kWaves * 64, ND <= 2 ? 2 : 1) void attention_tiled_
 #pragma unroll
         for (int i = 0; i < 16; i++) acc[t][i] *= f;
       m = to;
+      if (any_held && up) held[wave][r32] = make_float2(m, 0.0f);
     }
     return m == kMinusInf ? 0.0f : m;
   };

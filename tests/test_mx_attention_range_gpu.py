@@ -244,3 +244,24 @@ def test_large_scores(seqs, G, power, kind, fmt):
     want = np.where(np.arange(nq)[:, None, None] == nq - 1, v[-1], v[7])[:, :, None]
     # one weight, its sum and their quotient: exact but for two fp32 roundings and y's own
     assert (np.abs(y - want) <= rounding(kind, np.abs(want)) + 2 * U * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("kind,fmt", [("bf16", "fp8"), ("fp32", "fp4")])
+@pytest.mark.parametrize("nq", [1, 20])
+def test_large_and_small_values_within_shares(nq, kind, fmt):
+    """Runs of 192 keys of 2^120, zeros and ones, some of each in every share of a
+    sequence's keys: references fall within shares, and their parts are joined."""
+    from q4_packed_weight_amd import binding
+    nk, Hk = 12288, 48
+    b = Batch([(nq, nk)], Hk, 1, 32, 64, fmt, kind)
+    assert binding.mx_attention_workspace_size(b.T, Hk, Hk, 32, 1, b.width, 64, b.most) > 0
+    run = np.arange(nk) // 192 % 3
+    x = b.g.uniform(0.5, 1.0, (nk, Hk, 32))
+    values(b, 0, 2, x * np.array([2.0 ** 120, 0.0, 1.0])[run][:, None, None])
+    # heads by threes: the large values alone, none of them, all alike
+    side = np.array([-4.0, 4.0, 0.0])[np.arange(Hk) % 3][:, None]
+    values(b, 0, 0, np.where(run == 0, -1.0, 1.0)[:, None, None] * side * np.ones((nk, Hk, 32)))
+    b.pool.upload()
+    b.q, b.held = put(np.ones((b.T, Hk, 32)), kind)
+    b.scale = 75 / 128
+    check(b, b.run(causal=False), causal=False, tokens=sorted({0, nq - 1}))
