@@ -54,7 +54,7 @@ template <int LP> __device__ __forceinline__ uint32_t max_of_key(uint32_t v) {
 // The tile's references are those of the tiles before as long as they hold (stage
 // says so, stage_again mends it), so that nothing is exchanged before the barrier.
 // Bound by the waits of two waves a SIMD: of 2048 tokens over 8192 keys (32 heads of
-// 128, 241 GFLOP, 329 to 340 us by the card, 0.73 PFLOP/s, half of a large fp16
+// 128, 241 GFLOP, 330 to 348 us by the card, 0.7 PFLOP/s, half of a large fp16
 // product's rate) the matrix pipe works 28% and the vector unit 44% of the time.
 // Tried, when it took 322: operands read ahead in a fixed order, with the sums kept in
 // memory around that loop so that its registers suffice 361 us, without 390; 2 x 32-key
